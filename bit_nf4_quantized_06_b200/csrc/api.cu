@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/qlora.h"
+#include "host.h"
 #include "kernels.h"
 #include "nf4_dev.cuh"
 #include "ptx.cuh"
@@ -240,6 +241,7 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
 // The same device check every entry point runs first (see device_ready), for
 // the entry points defined in other files.
 int check_current_device_status() { return static_cast<int>(device_ready(nullptr)); }
+int check_current_device(int* sms) { return static_cast<int>(device_ready(sms)); }
 
 namespace {
 
@@ -394,6 +396,17 @@ inline qlora_status_t launch_status() {
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
+
+}  // namespace
+
+int launch_done() { return static_cast<int>(launch_status()); }
+
+bool encode_map2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+  return map2d(m, dt, ptr, inner, outer, row_bytes, box_inner, box_outer, sw);
+}
+
+namespace {
 
 CUtensorMap zero_map() {
   CUtensorMap m;

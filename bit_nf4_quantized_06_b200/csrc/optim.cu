@@ -14,6 +14,7 @@
 //   m <- b1 m + (1 - b1) g;  v <- b2 v + (1 - b2) g^2
 //   p <- p (1 - lr wd);      p <- p - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // and the bf16 copy the GEMMs read, if given, becomes bf16(p).
+#include "adamw_math.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -22,11 +23,8 @@ namespace qlora {
 namespace {
 
 __device__ __forceinline__ float adamw_one(float p, float g, float& m, float& v, const AdamwParams& a) {
-  m = fmaf(a.beta1, m, (1.0f - a.beta1) * g);
-  v = fmaf(a.beta2, v, (1.0f - a.beta2) * g * g);
-  p = p * a.decay;
-  const float denom = sqrtf(v) * a.inv_sqrt_bc2 + a.eps;
-  return p - a.step_size * (m / denom);
+  float root;
+  return adamw_update(p, g, m, v, root, a);
 }
 
 }  // namespace

@@ -1,0 +1,327 @@
+// AdamW over many tensors in one launch, states in 32 bits or in 8 (sm_100a).
+//
+// A stack's adapters are hundreds of tensors of 10^4 to 10^6 values: one
+// launch each costs more than the update. The descriptors travel as the
+// kernel's parameters (no copy, nothing left to keep alive, capturable), and
+// the CTAs walk the chunks of all tensors as one list.
+//
+// 8 bits: m and sqrt(v) are e4m3 codes with one fp32 scale per 256 values of
+// a tensor (fp8_dev.cuh); a warp owns a block, eight values a lane, so that
+// the block's maxima are warp shuffles. sqrt(v) rather than v: e4m3 spans
+// 2^17.8 from its smallest code to its largest, which is 2^35 of v. A code of
+// a value above zero is not allowed to become zero, else the next step would
+// divide by eps alone. The step uses the new m and v in fp32, so rounding
+// them to 8 bits acts on later steps only.
+//
+// Bound by HBM: 30 bytes a value (32 bits, with the bf16 copy) or 18.1 (8 bits).
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include <cuda_bf16.h>
+
+#include "../../include/qlora.h"
+#include "adamw_math.cuh"
+#include "fp8_dev.cuh"
+#include "host.h"
+#include "ptx.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kStateBlock = QLORA_ADAMW_STATE_BLOCK;
+constexpr int kThreads = 256;
+constexpr int kChunkValues = 4096;   // values of one chunk: a CTA's unit of work
+constexpr float kLeastRoot = 1.0f / 512.0f;   // the smallest e4m3 code above zero
+
+struct MultiTensor {
+  float* master;
+  __nv_bfloat16* param;
+  const float* grad;
+  void* m;
+  void* v;
+  float* m_scales;
+  float* v_scales;
+  int64_t n;
+};
+
+// Up to CAP tensors: two capacities, so that a few tensors do not pay for the
+// copy of a 32 KB parameter block at launch.
+template <int CAP>
+struct Multi {
+  MultiTensor t[CAP];
+  int32_t first[CAP];       // the tensor's first chunk; bit 31: wide loads allowed
+  int32_t count;
+  int32_t chunks;
+  AdamwHyper hp;
+};
+constexpr int kCapSmall = 24, kCapLarge = 470;
+static_assert(sizeof(Multi<kCapLarge>) <= 32764, "kernel parameter block");
+
+__device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, bool vec, const AdamwHyper& hp) {
+  // values i0 + 8 lane + j of the block that starts at i0
+  const int64_t at = i0 + 8 * lane;
+  const int64_t blk = i0 / kStateBlock;
+  const int valid = static_cast<int>(min(static_cast<int64_t>(8), max(static_cast<int64_t>(0), t.n - at)));
+  const float ms = t.m_scales[blk], vs = t.v_scales[blk];
+  uint8_t* mc = static_cast<uint8_t*>(t.m) + at;
+  uint8_t* vc = static_cast<uint8_t*>(t.v) + at;
+  float p[8], g[8], m[8], r[8];
+  const bool wide = vec && valid == 8;
+  uint2 mq = make_uint2(0, 0), vq = make_uint2(0, 0);
+  if (wide) {
+    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(t.master + at);
+    *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(t.master + at + 4);
+    *reinterpret_cast<float4*>(g) = __ldcs(reinterpret_cast<const float4*>(t.grad + at));
+    *reinterpret_cast<float4*>(g + 4) = __ldcs(reinterpret_cast<const float4*>(t.grad + at + 4));
+    mq = *reinterpret_cast<const uint2*>(mc);
+    vq = *reinterpret_cast<const uint2*>(vc);
+  } else {
+    uint32_t mb[8], vb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool ok = j < valid;
+      p[j] = ok ? t.master[at + j] : 0.0f;
+      g[j] = ok ? t.grad[at + j] : 0.0f;
+      mb[j] = ok ? mc[j] : 0u;
+      vb[j] = ok ? vc[j] : 0u;
+    }
+    mq = make_uint2(mb[0] | mb[1] << 8 | mb[2] << 16 | mb[3] << 24, mb[4] | mb[5] << 8 | mb[6] << 16 | mb[7] << 24);
+    vq = make_uint2(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24, vb[4] | vb[5] << 8 | vb[6] << 16 | vb[7] << 24);
+  }
+  float am = 0.0f, av = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint32_t sh = 8 * (j & 3);
+    const float2 mm = fp8_unpack2<kE4M3>((j < 4 ? mq.x : mq.y) >> sh);
+    const float2 rr = fp8_unpack2<kE4M3>((j < 4 ? vq.x : vq.y) >> sh);
+    m[j] = mm.x * ms;
+    m[j + 1] = mm.y * ms;
+    r[j] = rr.x * vs;
+    r[j + 1] = rr.y * vs;
+#pragma unroll
+    for (int e = j; e < j + 2; ++e) {
+      float v = r[e] * r[e];
+      p[e] = adamw_update(p[e], g[e], m[e], v, r[e], hp);
+      am = fmaxf(am, fp8_mag(m[e]));
+      av = fmaxf(av, fp8_mag(r[e]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+    av = fmaxf(av, __shfl_xor_sync(0xFFFFFFFFu, av, o));
+  }
+  constexpr float F = 448.0f;
+  am = fmaxf(am, kFp8Least);
+  av = fmaxf(av, kFp8Least);
+  const float im = F / am, iv = F / av;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    m[j] = fp8_scaled(m[j], im);
+    const float c = r[j] * iv;
+    r[j] = (r[j] > 0.0f ? fmaxf(c, kLeastRoot) : c) + (r[j] - r[j]);   // NaN where the root is not finite
+  }
+  mq = make_uint2(fp8_pack4<kE4M3>(m[0], m[1], m[2], m[3]), fp8_pack4<kE4M3>(m[4], m[5], m[6], m[7]));
+  vq = make_uint2(fp8_pack4<kE4M3>(r[0], r[1], r[2], r[3]), fp8_pack4<kE4M3>(r[4], r[5], r[6], r[7]));
+  if (lane == 0) {
+    t.m_scales[blk] = am / F;
+    t.v_scales[blk] = av / F;
+  }
+  if (wide) {
+    *reinterpret_cast<float4*>(t.master + at) = *reinterpret_cast<const float4*>(p);
+    *reinterpret_cast<float4*>(t.master + at + 4) = *reinterpret_cast<const float4*>(p + 4);
+    *reinterpret_cast<uint2*>(mc) = mq;
+    *reinterpret_cast<uint2*>(vc) = vq;
+    if (t.param != nullptr)
+      *reinterpret_cast<uint4*>(t.param + at) = make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
+                                                           pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= valid) continue;
+      t.master[at + j] = p[j];
+      mc[j] = static_cast<uint8_t>((j < 4 ? mq.x : mq.y) >> (8 * (j & 3)));
+      vc[j] = static_cast<uint8_t>((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
+      if (t.param != nullptr) t.param[at + j] = __float2bfloat16_rn(p[j]);
+    }
+  }
+}
+
+__device__ __forceinline__ void step32(const MultiTensor& t, int64_t at, bool vec, const AdamwHyper& hp) {
+  float* m = static_cast<float*>(t.m);
+  float* v = static_cast<float*>(t.v);
+  if (at >= t.n) return;
+  float root;
+  if (vec && at + 4 <= t.n) {
+    float4 p4 = *reinterpret_cast<const float4*>(t.master + at);
+    const float4 g4 = __ldcs(reinterpret_cast<const float4*>(t.grad + at));
+    float4 m4 = *reinterpret_cast<const float4*>(m + at);
+    float4 v4 = *reinterpret_cast<const float4*>(v + at);
+    p4.x = adamw_update(p4.x, g4.x, m4.x, v4.x, root, hp);
+    p4.y = adamw_update(p4.y, g4.y, m4.y, v4.y, root, hp);
+    p4.z = adamw_update(p4.z, g4.z, m4.z, v4.z, root, hp);
+    p4.w = adamw_update(p4.w, g4.w, m4.w, v4.w, root, hp);
+    *reinterpret_cast<float4*>(t.master + at) = p4;
+    *reinterpret_cast<float4*>(m + at) = m4;
+    *reinterpret_cast<float4*>(v + at) = v4;
+    if (t.param != nullptr)
+      *reinterpret_cast<uint2*>(t.param + at) = make_uint2(pack_bf16x2(p4.x, p4.y), pack_bf16x2(p4.z, p4.w));
+    return;
+  }
+  for (int64_t i = at; i < min(at + 4, t.n); ++i) {
+    float mi = m[i], vi = v[i];
+    const float p = adamw_update(t.master[i], t.grad[i], mi, vi, root, hp);
+    t.master[i] = p;
+    m[i] = mi;
+    v[i] = vi;
+    if (t.param != nullptr) t.param[i] = __float2bfloat16_rn(p);
+  }
+}
+
+template <int CAP, bool BITS8>
+__global__ void __launch_bounds__(kThreads) k_adamw_multi(const __grid_constant__ Multi<CAP> a) {
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+    // the last tensor whose first chunk is not past c
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((a.first[mid] & 0x7FFFFFFF) <= c)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const MultiTensor& t = a.t[lo];
+    const bool vec = a.first[lo] < 0;
+    const int64_t i0 = static_cast<int64_t>(c - (a.first[lo] & 0x7FFFFFFF)) * kChunkValues;
+    if (BITS8) {
+#pragma unroll
+      for (int s = 0; s < kChunkValues / (kThreads * 8); ++s) {
+        const int64_t b0 = i0 + (s * (kThreads / 32) + warp) * kStateBlock;
+        if (b0 < t.n) step8(t, b0, lane, vec, a.hp);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kChunkValues / (kThreads * 4); ++s)
+        step32(t, i0 + (s * kThreads + threadIdx.x) * 4, vec, a.hp);
+    }
+  }
+}
+
+using host::aligned;
+using host::cdiv;
+
+template <int CAP, bool BITS8>
+int launch_multi(const qlora_adamw_tensor_t* t, const int* index, int count, const AdamwHyper& hp, int sms,
+                 cudaStream_t st) {
+  Multi<CAP> a;
+  a.count = count;
+  a.hp = hp;
+  int64_t chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    const qlora_adamw_tensor_t& s = t[index[i]];
+    a.t[i] = MultiTensor{s.master, static_cast<__nv_bfloat16*>(s.param_bf16), s.grad, s.m, s.v,
+                         s.m_scales, s.v_scales, s.n};
+    const unsigned state = BITS8 ? 8 : 16, copy = BITS8 ? 16 : 8;
+    const bool vec = aligned(s.master, 16) && aligned(s.grad, 16) && aligned(s.m, state) && aligned(s.v, state) &&
+                     aligned(s.param_bf16, copy);
+    a.first[i] = static_cast<int32_t>(chunks) | (vec ? static_cast<int32_t>(0x80000000u) : 0);
+    chunks += cdiv(s.n, kChunkValues);
+  }
+  a.chunks = static_cast<int32_t>(chunks);
+  const int grid = static_cast<int>(std::min<int64_t>(chunks, static_cast<int64_t>(sms) * 8));
+  return host::launch_pdl(k_adamw_multi<CAP, BITS8>, dim3(grid), dim3(kThreads), 0, st, 1, a);
+}
+
+// Whether two of the ranges [at(i), at(i) + bytes(i)) of the listed tensors overlap.
+template <typename At, typename Bytes>
+bool overlap(const std::vector<int>& live, At at, Bytes bytes) {
+  bool ascending = true;
+  for (size_t i = 1; ascending && i < live.size(); ++i)
+    ascending = at(live[i - 1]) + bytes(live[i - 1]) <= at(live[i]);
+  if (ascending) return false;     // the usual case: laid out one after the other
+  std::vector<std::pair<uintptr_t, uintptr_t>> r;
+  r.reserve(live.size());
+  for (int i : live) r.emplace_back(at(i), at(i) + bytes(i));
+  std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].second) return true;
+  return false;
+}
+
+}  // namespace
+}  // namespace qlora
+
+using namespace qlora;
+
+extern "C" qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t* tensors, int64_t count, int32_t state_bits,
+                                            const qlora_adamw_t* hp, void* stream) {
+  if (hp == nullptr || count < 0 || (count > 0 && tensors == nullptr) || (state_bits != 8 && state_bits != 32))
+    return QLORA_ERR_INVALID_ARG;
+  if (count > (int64_t(1) << 24)) return QLORA_ERR_SHAPE;
+  if (hp->step < 1 || !(hp->lr >= 0.0f) || !std::isfinite(hp->lr) || !(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) ||
+      !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f) || !(hp->eps > 0.0f) || !std::isfinite(hp->eps) ||
+      !std::isfinite(hp->weight_decay))
+    return QLORA_ERR_INVALID_ARG;
+  const bool b8 = state_bits == 8;
+  try {
+    std::vector<int> live;
+    live.reserve(static_cast<size_t>(count));
+    for (int64_t i = 0; i < count; ++i) {
+      const qlora_adamw_tensor_t& t = tensors[i];
+      if (t.n < 0 || t.n > (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
+      if (t.n == 0) continue;
+      if (t.master == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr ||
+          (b8 && (t.m_scales == nullptr || t.v_scales == nullptr)))
+        return QLORA_ERR_INVALID_ARG;
+      if (!aligned(t.master, 4) || !aligned(t.grad, 4) || !aligned(t.param_bf16, 2) ||
+          (b8 ? !aligned(t.m_scales, 4) || !aligned(t.v_scales, 4) : !aligned(t.m, 4) || !aligned(t.v, 4)))
+        return QLORA_ERR_ALIGNMENT;
+      live.push_back(static_cast<int>(i));
+    }
+    if (live.empty()) return QLORA_OK;
+    const size_t w = b8 ? 1 : 4;
+    auto addr = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+    auto n = [&](int i) { return static_cast<uintptr_t>(tensors[i].n); };
+    if (overlap(live, [&](int i) { return addr(tensors[i].master); }, [&](int i) { return 4 * n(i); }) ||
+        overlap(live, [&](int i) { return addr(tensors[i].m); }, [&](int i) { return w * n(i); }) ||
+        overlap(live, [&](int i) { return addr(tensors[i].v); }, [&](int i) { return w * n(i); }))
+      return QLORA_ERR_INVALID_ARG;
+    int sms = 0;
+    qlora_status_t s = static_cast<qlora_status_t>(check_current_device(&sms));
+    if (s != QLORA_OK) return s;
+    // step constants in double, rounded once, as qlora_adamw_step has them
+    AdamwHyper h{};
+    h.beta1 = hp->beta1;
+    h.beta2 = hp->beta2;
+    h.eps = hp->eps;
+    h.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
+    h.step_size = static_cast<float>(hp->lr / (1.0 - std::pow(static_cast<double>(hp->beta1), hp->step)));
+    h.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(hp->beta2), hp->step)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // as many tensors a launch as its parameter block and 31-bit chunk numbers hold
+    for (size_t at = 0; at < live.size();) {
+      size_t to = at;
+      int64_t chunks = 0;
+      while (to < live.size() && to - at < kCapLarge) {
+        const int64_t more = cdiv(tensors[live[to]].n, kChunkValues);
+        if (to > at && chunks + more > (int64_t(1) << 30)) break;
+        chunks += more;
+        ++to;
+      }
+      const int k = static_cast<int>(to - at);
+      const int rc = k <= kCapSmall ? (b8 ? launch_multi<kCapSmall, true>(tensors, &live[at], k, h, sms, st)
+                                          : launch_multi<kCapSmall, false>(tensors, &live[at], k, h, sms, st))
+                                    : (b8 ? launch_multi<kCapLarge, true>(tensors, &live[at], k, h, sms, st)
+                                          : launch_multi<kCapLarge, false>(tensors, &live[at], k, h, sms, st));
+      if (rc != QLORA_OK) return static_cast<qlora_status_t>(rc);
+      at = to;
+    }
+  } catch (...) {   // only the host vectors' memory can fail
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
+}

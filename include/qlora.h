@@ -49,7 +49,9 @@
  *   - Kernels never wait without a bound: a pipeline wait that exceeds about
  *     two seconds ends the kernel and sets a device status bit that
  *     qlora_device_status() reports as QLORA_ERR_TIMEOUT.
- *   - Inputs must be finite; results for non-finite weights are unspecified.
+ *   - Inputs must be finite; results for non-finite weights are unspecified
+ *     (the 8-bit linear, the RMS norm and the many-tensor AdamW state what
+ *     they do with values that are not finite).
  */
 #ifndef QLORA_H_
 #define QLORA_H_
@@ -299,6 +301,130 @@ QLORA_API qlora_status_t qlora_adamw_paged(const float *grad_dev, void *param_de
 QLORA_API qlora_status_t qlora_adamw_staged(float *master, void *param_bf16, const float *grad, float *m_host,
                                             float *v_host, float *m_stage, float *v_stage, int64_t n,
                                             const qlora_adamw_t *hp, void *stream);
+
+/* ------------------------------------------------------------------ 8-bit linear
+ * A frozen weight without adapters of its own (a merged one from
+ * qlora_merge_lora, or a projection that is not adapted) can be kept in 8-bit
+ * floating point. Block quantization, used for weights, activations and
+ * gradients alike, with F = 448 (e4m3) or 57344 (e5m2):
+ *   amax  = max over the block's finite |v|, at least 2^-100
+ *   scale = fl32(amax / F)
+ *   code  = fp8_rn(clamp(fl32(v * fl32(F / amax)), -F, F))
+ * An infinite or NaN value becomes the NaN code and does not enter amax, so
+ * it spoils only the results that it takes part in.
+ *   weight: 128 x 128 blocks, e4m3; the last blocks of either axis are short
+ *   rows:   blocks of 128 consecutive columns of one row, e4m3 or e5m2
+ * Products of codes are summed in fp32 within a block of 128 of the
+ * reduction, multiplied by the two scales, and summed over blocks in fp32. */
+typedef enum { QLORA_FP8_E4M3 = 0, QLORA_FP8_E5M2 = 1 } qlora_fp8_format_t;
+
+/* Weight in e4m3, row-major, caller-owned device buffers. */
+typedef struct {
+  int64_t n_out;   /* N rows                                                  */
+  int64_t k_in;    /* K columns, K % 16 == 0                                  */
+  uint8_t *codes;  /* [N x K], 16-byte aligned                                */
+  float *scales;   /* [ceil(N/128) x ceil(K/128)]                             */
+} qlora_fp8_t;
+
+/* Rows (tokens) in 8 bits, caller-owned device buffers. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;      /* bytes from row to row: a multiple of 16, >= cols; bytes
+                      past cols are neither read nor written               */
+  uint8_t *codes;  /* rows of cols codes, 16-byte aligned                     */
+  float *scales;   /* [rows x ceil(cols/128)]                                 */
+  int32_t format;  /* qlora_fp8_format_t                                      */
+  int32_t reserved;/* must be 0                                               */
+} qlora_fp8_rows_t;
+
+/* Quantize a bf16 weight W [N x K] (device) into q. */
+QLORA_API qlora_status_t qlora_quantize_fp8(const void *w_bf16, const qlora_fp8_t *q, void *stream);
+
+/* w_out [N x K] bf16 = bf16(code * scale). */
+QLORA_API qlora_status_t qlora_dequantize_fp8(const qlora_fp8_t *q, void *w_bf16_out, void *stream);
+
+/* Quantize bf16 rows x [rows x cols] (dense) into out. rows == 0 is a no-op. */
+QLORA_API qlora_status_t qlora_quantize_fp8_rows(const void *x_bf16, const qlora_fp8_rows_t *out, void *stream);
+
+/* Workspace bytes for qlora_fp8_linear_fwd and _bwd at these sizes (the rows
+ * in 8 bits where they come in bf16, and fp32 partial sums where the
+ * reduction is split over SMs); 0 for sizes out of range. Depends on the
+ * current device's SM count. */
+QLORA_API size_t qlora_fp8_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in);
+
+/* y [m x N] bf16 = x W^T. x comes either as bf16 [m x K] (quantized to e4m3
+ * rows within the call) or as rows already in 8 bits (x8: m rows of K);
+ * exactly one of the two is given. m == 0 is a no-op. */
+QLORA_API qlora_status_t qlora_fp8_linear_fwd(const qlora_fp8_t *q, const void *x_bf16, const qlora_fp8_rows_t *x8,
+                                              int64_t m, void *y_bf16, void *ws, size_t ws_bytes, void *stream);
+
+/* dX [m x K] bf16 = dY W; no gradient into W. dY comes as bf16 [m x N]
+ * (quantized to rows of `format` within the call) or as rows already in
+ * 8 bits (dy8: m rows of N; `format` is then ignored). m == 0 is a no-op. */
+QLORA_API qlora_status_t qlora_fp8_linear_bwd(const qlora_fp8_t *q, const void *dy_bf16, const qlora_fp8_rows_t *dy8,
+                                              int32_t format, int64_t m, void *dx_bf16, void *ws, size_t ws_bytes,
+                                              void *stream);
+
+/* ------------------------------------------------------------------ RMS norm
+ * The norm in front of a projection, with the residual's addition:
+ *   h    = bf16(x + residual)   (h = x without a residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps), per row, fp32
+ *   y    = h rstd gamma
+ * x, residual [rows x d], gamma [d] bf16. y goes to y_bf16 (one rounding) or,
+ * as 8-bit rows for qlora_fp8_linear_fwd, to y8 (e4m3 or e5m2); exactly one is
+ * given. h_out [rows x d] bf16 receives h where there is a residual (NULL
+ * without one); it may be x's or the residual's own buffer. rstd_out [rows]
+ * may be NULL. No other buffers may overlap. rows == 0 is a no-op; d >= 1;
+ * eps >= 0 and finite. A row of zeros with eps 0 gives NaN, as the formula. */
+QLORA_API qlora_status_t qlora_rmsnorm_fwd(const void *x_bf16, const void *residual_bf16, const void *gamma_bf16,
+                                           int64_t rows, int64_t d, float eps, void *h_out_bf16, void *y_bf16,
+                                           const qlora_fp8_rows_t *y8, float *rstd_out, void *stream);
+
+/* Workspace bytes for qlora_rmsnorm_bwd (fp32 partial sums of dgamma). */
+QLORA_API size_t qlora_rmsnorm_workspace_bytes(int64_t rows, int64_t d);
+
+/* Gradients of y = h rstd gamma (rstd [rows] as the forward wrote it):
+ *   dx [rows x d] bf16 = rstd (dy gamma - h rstd^2 mean(dy gamma h)) + dres
+ *   dgamma [d] fp32    = sum over rows of dy h rstd (overwritten; NULL to skip)
+ * dres [rows x d] bf16, the gradient that reaches h past the norm, may be
+ * NULL; dx is the gradient of x and of the residual alike and may be dres's or
+ * dy's own buffer. Sums run in a fixed order: results repeat bit for bit.
+ * rows == 0 zeroes dgamma. */
+QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void *dy_bf16, const void *h_bf16, const void *gamma_bf16,
+                                           const float *rstd, const void *dres_bf16, int64_t rows, int64_t d,
+                                           void *dx_bf16, float *dgamma, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ AdamW over many tensors
+ * The update of qlora_adamw_step for `count` tensors in few launches (all
+ * adapters and norm gains of a model), with states in 32 bits or in 8.
+ *   state_bits 32: m, v fp32 [n]; m_scales, v_scales unused.
+ *   state_bits 8:  m holds e4m3 codes [n] of m and v e4m3 codes [n] of
+ *     sqrt(v), quantized as above in blocks of 256 consecutive values of the
+ *     tensor (scales [ceil(n/256)] each; all zero bytes mean zero states). A
+ *     sqrt(v) above zero keeps a code above zero (at least 2^-9), so that no
+ *     step divides by eps alone. The root halves the exponent range that v
+ *     needs. A gradient that is not finite spoils its own value only, as with
+ *     32-bit states. The step itself uses the new m and v before they are
+ *     rounded to 8 bits.
+ * `tensors` is a host array; it is read during the call and may be reused at
+ * once. Buffers of different tensors must not overlap: the same master, m or
+ * v twice is refused. n == 0 entries are skipped. fp32 pointers 4-byte,
+ * param_bf16 (may be NULL) 2-byte aligned; tensors with 16-byte aligned
+ * buffers (8-byte for bf16 and codes) take the wide loads. */
+typedef struct {
+  float *master;
+  void *param_bf16;
+  const float *grad;
+  void *m;
+  void *v;
+  float *m_scales;
+  float *v_scales;
+  int64_t n;
+} qlora_adamw_tensor_t;
+#define QLORA_ADAMW_STATE_BLOCK 256
+QLORA_API qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t *tensors, int64_t count, int32_t state_bits,
+                                           const qlora_adamw_t *hp, void *stream);
 
 /* Synchronises `stream`, then reads and clears the device status word of the
  * current device. Returns QLORA_OK, QLORA_ERR_TIMEOUT (a kernel gave up on a

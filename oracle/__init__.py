@@ -30,6 +30,9 @@ Modules
 ``linear``  forward and backward of the quantized linear in fp64.
 ``brute``   literal pure-Python loops for tiny inputs (pins ``nf4``).
 ``bf16``    float32 <-> bfloat16 round-to-nearest-even bit helpers.
+``fp8``     8-bit floating point (e4m3, e5m2) and its block quantization.
+``norm``    RMS norm and its gradients in fp64.
+``optim``   AdamW in fp64.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test
 against something other than itself (closed forms, brute force, finite
