@@ -227,6 +227,7 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_merge_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(merge_tc_smem_bytes()));
+    if (e == cudaSuccess) e = set_fp8_attributes();
     if (e != cudaSuccess) return QLORA_ERR_CUDA;
     st.attrs = true;
     st.ctx = ctx;
@@ -241,7 +242,7 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
 // The same device check every entry point runs first (see device_ready), for
 // the entry points defined in other files.
 int check_current_device_status() { return static_cast<int>(device_ready(nullptr)); }
-int check_current_device(int* sms) { return static_cast<int>(device_ready(sms)); }
+int check_current_device(int* sms, int* pairs) { return static_cast<int>(device_ready(sms, pairs)); }
 
 namespace {
 

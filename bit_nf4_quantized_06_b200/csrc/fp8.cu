@@ -5,11 +5,13 @@
 //   dX[m][k] = sum_b sd[m][b] sw[b][k/128] sum_{n in b} d[m][n] w[n][k]
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include <cuda_bf16.h>
 
 #include "../../include/qlora.h"
 #include "fp8_dev.cuh"
+#include "fp8_pair.h"
 #include "host.h"
 #include "ptx.cuh"
 
@@ -177,6 +179,35 @@ qlora_status_t check_weight(const qlora_fp8_t* q) {
   return QLORA_OK;
 }
 
+template <bool BWD>
+int launch_pair_product(const Product& p, int format, int pairs, cudaStream_t st) {
+  Fp8Gemm g{};
+  g.sx = p.sx;
+  g.sw = p.sw;
+  g.y = p.y;
+  g.xblk = p.xblk;
+  g.sw_out = BWD ? 1 : p.nbk;
+  g.sw_red = BWD ? p.nbk : 1;
+  g.m = static_cast<int32_t>(p.m);
+  g.cols = static_cast<int32_t>(p.cols);
+  g.kblocks = static_cast<int32_t>(p.xblk);
+  g.tiles_m = static_cast<int32_t>(cdiv(p.m, 256));
+  g.tiles_n = static_cast<int32_t>(cdiv(p.cols, 256));
+  g.a_format = format;
+  g.tma_out = p.cols % 8 == 0;
+  CUtensorMap x, w, o;
+  std::memset(&o, 0, sizeof(o));
+  const int64_t n = BWD ? p.red : p.cols;
+  if (!encode_map2d(&x, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x, p.red, p.m, p.ldx, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.k, n, p.k, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (g.tma_out && !encode_map2d(&o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.y, p.cols, p.m, p.cols * 2, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_64B)))
+    return QLORA_ERR_CUDA;
+  const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
+  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
+  return host::launch_pdl(k_fp8_pair<BWD>, dim3(grid), dim3(320), kFp8PairSmem, st, 2, x, w, o, g);
+}
+
 // Workspace of a product over rows of `red` values: the rows' codes and scales.
 struct ProductPlan {
   size_t codes, scales, total;
@@ -205,8 +236,8 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
   if (m == 0) return QLORA_OK;
   if ((x_bf16 == nullptr) == (x8 == nullptr) || out_bf16 == nullptr) return QLORA_ERR_INVALID_ARG;
   if (!aligned(x_bf16, 16) || !aligned(out_bf16, 16) || !aligned(ws, 16)) return QLORA_ERR_ALIGNMENT;
-  int sms = 0;
-  if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
+  int sms = 0, pairs = 0;
+  if ((s = static_cast<qlora_status_t>(check_current_device(&sms, &pairs))) != QLORA_OK) return s;
   qlora_fp8_rows_t rows;
   if (x8 != nullptr) {
     rows = *x8;
@@ -220,6 +251,7 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
   }
   Product p{rows.codes, rows.scales, q->codes, q->scales, static_cast<__nv_bfloat16*>(out_bf16), m, cols, red,
             rows.ld, cdiv(red, kFp8Block), q->k_in, cdiv(q->k_in, kFp8Block)};
+  if (m > 128) return static_cast<qlora_status_t>(launch_pair_product<BWD>(p, rows.format, pairs, st));
   const dim3 grid(static_cast<unsigned>(cdiv(cols, 64)), static_cast<unsigned>(cdiv(m, 64)));
   return static_cast<qlora_status_t>(
       rows.format == QLORA_FP8_E5M2 ? host::launch_pdl(k_fp8_product<BWD, kE5M2>, grid, dim3(256), 0, st, 1, p)
@@ -227,6 +259,14 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
 }
 
 }  // namespace
+
+cudaError_t set_fp8_attributes() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_fp8_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFp8PairSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_fp8_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFp8PairSmem);
+}
+
 }  // namespace qlora
 
 using namespace qlora;

@@ -1,0 +1,58 @@
+// Tensor-core product of 8-bit rows with an 8-bit weight: parameters and
+// helpers shared by the CTA-pair kernel and the split kernel.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "fp8_dev.cuh"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+
+namespace qlora {
+
+struct Fp8Gemm {
+  const float* sx;          // [m x xblk] scales of the rows
+  const float* sw;          // scales of the weight, at output block * sw_out + reduction block * sw_red
+  __nv_bfloat16* y;         // [m x cols]
+  int64_t xblk, sw_out, sw_red;
+  int32_t m, cols;
+  int32_t kblocks;          // reduction blocks of 128
+  int32_t tiles_m, tiles_n;
+  int32_t a_format;         // format of the rows' codes (Fp8Format)
+  int32_t tma_out;          // output through TMA stores (cols % 8 == 0)
+};
+
+// Instruction descriptor for kind::f8f6f4: A e4m3 or e5m2, B e4m3, fp32 D.
+__device__ __forceinline__ uint32_t idesc_fp8(int m, int n, int a_format, bool b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(a_format) << 7) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns: thread i gets lane i.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// acc[16 chunk + 2i, +1] += t[2i, 2i+1] * s
+__device__ __forceinline__ void promote16(uint64_t* acc, const uint32_t (&t)[16], uint64_t s2) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = f2_fma(f2(__uint_as_float(t[2 * i]), __uint_as_float(t[2 * i + 1])), s2, acc[i]);
+}
+
+}  // namespace qlora

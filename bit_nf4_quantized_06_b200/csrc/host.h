@@ -10,8 +10,12 @@
 namespace qlora {
 
 // Device check of the current device (see check_current_device_status), with
-// its SM count.
-int check_current_device(int* sms);
+// its SM count and how many CTA pairs of one CTA a SM fit on it at once.
+int check_current_device(int* sms, int* pairs = nullptr);
+
+// Shared-memory limits of the 8-bit product's kernels (fp8.cu); part of the
+// device check, which sets every kernel's attributes once a context.
+cudaError_t set_fp8_attributes();
 
 // Counts a launch and returns its status (a qlora_status_t).
 int launch_done();
