@@ -205,7 +205,7 @@ int launch_pair_product(const Product& p, int format, int pairs, cudaStream_t st
     return QLORA_ERR_CUDA;
   const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
-  return host::launch_pdl(k_fp8_pair<BWD>, dim3(grid), dim3(320), kFp8PairSmem, st, 2, x, w, o, g);
+  return host::launch_pdl(k_fp8_pair<BWD>, dim3(grid), dim3(kFp8PairThreads), kFp8PairSmem, st, 2, x, w, o, g);
 }
 
 // Workspace of a product over rows of `red` values: the rows' codes and scales.

@@ -22,6 +22,24 @@ struct Fp8Gemm {
   int32_t tma_out;          // output through TMA stores (cols % 8 == 0)
 };
 
+// The bounded waits of ptx.cuh after a number of plain tries: the timer of
+// the bound is slow to read next to a step of this pipeline (512 cycles), and
+// most waits end within a few tries.
+constexpr int kPlainTries = 256;
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
+#pragma unroll 1
+  for (int i = 0; i < kPlainTries; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, code);
+}
+__device__ __forceinline__ bool fp8_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                 unsigned code) {
+#pragma unroll 1
+  for (int i = 0; i < kPlainTries; ++i)
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+  return mbar_wait_cluster(bar, parity, abort_flag, code);
+}
+
 // Instruction descriptor for kind::f8f6f4: A e4m3 or e5m2, B e4m3, fp32 D.
 __device__ __forceinline__ uint32_t idesc_fp8(int m, int n, int a_format, bool b_mn_major) {
   return (1u << 4) | (static_cast<uint32_t>(a_format) << 7) | ((b_mn_major ? 1u : 0u) << 16) |
@@ -38,6 +56,39 @@ __device__ __forceinline__ void tc_mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc
       : "memory");
 }
 
+// Arrive once on the barrier at this offset in both CTAs of the pair when
+// every MMA issued so far by this thread completes.
+__device__ __forceinline__ void tc_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 32 lanes x 16 consecutive 32-bit columns: thread i gets lane i.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -49,10 +100,11 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// acc[16 chunk + 2i, +1] += t[2i, 2i+1] * s
-__device__ __forceinline__ void promote16(uint64_t* acc, const uint32_t (&t)[16], uint64_t s2) {
+// acc[i] += t[i] * s. Plain FMAs: packed in pairs they took a register move a
+// value on the way.
+__device__ __forceinline__ void promote16(float* acc, const uint32_t (&t)[16], float s) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = f2_fma(f2(__uint_as_float(t[2 * i]), __uint_as_float(t[2 * i + 1])), s2, acc[i]);
+  for (int i = 0; i < 16; ++i) acc[i] = fmaf(__uint_as_float(t[i]), s, acc[i]);
 }
 
 }  // namespace qlora

@@ -31,7 +31,7 @@ namespace qlora {
 using namespace tcd;
 
 template <bool W_MN>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kFp8PairThreads, 1)
     k_fp8_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ CUtensorMap tm_out, Fp8Gemm p) {
   constexpr int STAGES = kFp8PairStages;
@@ -41,15 +41,18 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t boxes = base + STAGES * STAGE_BYTES;
-  const uint32_t bar0 = boxes + kFp8PairBoxes;
+  const uint32_t ring = boxes + kFp8PairBoxes;
+  const uint32_t bar0 = ring + kFp8PairRing;
   uint8_t* const ctl = smem_raw + (bar0 - raw);
   auto bar_full = [&](int s) { return bar0 + 8u * s; };                  // even CTA: loads of both
   auto bar_empty = [&](int s) { return bar0 + 8u * (STAGES + s); };      // local, from the MMA
   auto bar_accf = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };   // local, from the MMA
-  auto bar_acce = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };   // even CTA: 16 epilogue warps
-  const uint32_t bar_fin = bar0 + 8u * (2 * STAGES + 4);
-  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(ctl + 8 * (2 * STAGES + 5));
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * (2 * STAGES + 5) + 4);
+  auto bar_acce = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };   // even CTA: 32 epilogue warps
+  auto bar_sf = [&](int c) { return bar0 + 8u * (2 * STAGES + 4 + c); };     // two scale warps
+  auto bar_se = [&](int c) { return bar0 + 8u * (2 * STAGES + 6 + c); };     // 16 epilogue warps
+  const uint32_t bar_fin = bar0 + 8u * (2 * STAGES + 8);
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(ctl + 8 * (2 * STAGES + 9));
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * (2 * STAGES + 9) + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -66,7 +69,9 @@ __global__ void __launch_bounds__(320, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_accf(b), 1);
-      mbar_init(bar_acce(b), 16);
+      mbar_init(bar_acce(b), 32);
+      mbar_init(bar_sf(b), 2);
+      mbar_init(bar_se(b), 16);
     }
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
@@ -83,6 +88,9 @@ __global__ void __launch_bounds__(320, 1)
   grid_dependency_wait();
   grid_dependency_trigger();
 
+  // registers move from the first warpgroup to the epilogue's four (both
+  // sides' sum stays below the launch's)
+  if (warp < 4) setmaxnreg_dec<kFp8PairIssueRegs>();
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&tm_x);
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(320, 1)
         const int out = (tile / p.tiles_m) * 256 + 128 * rank;
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const int s = it % STAGES;
-          if (!mbar_wait(bar_empty(s), ((it / STAGES) & 1) ^ 1, abort_flag, QLORA_DEV_TIMEOUT_PRODUCER)) {
+          if (!fp8_wait(bar_empty(s), ((it / STAGES) & 1) ^ 1, abort_flag, QLORA_DEV_TIMEOUT_PRODUCER)) {
             ok = false;
             break;
           }
@@ -112,65 +120,121 @@ __global__ void __launch_bounds__(320, 1)
       for (int j = max(0, it - STAGES); j < it; ++j) drain_wait(bar_empty(j % STAGES), (j / STAGES) & 1);
     }
   } else if (warp == 1) {
-    if (leader && lane == 0) {
+    // the whole warp runs the loop, so that everything the MMAs take is uniform
+    // over the warp; one elected lane issues
+    if (leader) {
       const uint32_t idesc = idesc_fp8(256, 256, p.a_format, W_MN);
-      int it = 0;
+      const uint64_t dx0 = smem_desc_sw128(base, 16, 1024);
+      const uint64_t dw0 = W_MN ? smem_desc_sw128(base + HALF, HALF, 1024) : smem_desc_sw128(base + HALF, 16, 1024);
+      int s = 0, b = 0;
+      uint32_t ph = 0, aph = 1;     // parities of the stage and of the buffer
       bool ok = true;
       for (int tile = pair; ok && tile < ntiles; tile += npairs) {
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const int s = it % STAGES, b = it & 1;
-          if (!mbar_wait_cluster(bar_acce(b), ((it >> 1) & 1) ^ 1, abort_flag, QLORA_DEV_TIMEOUT_MMA) ||
-              !mbar_wait(bar_full(s), (it / STAGES) & 1, abort_flag, QLORA_DEV_TIMEOUT_MMA)) {
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!fp8_wait(bar_acce(b), aph, abort_flag, QLORA_DEV_TIMEOUT_MMA) ||
+              !fp8_wait(bar_full(s), ph, abort_flag, QLORA_DEV_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t x_s = base + s * STAGE_BYTES, w_s = x_s + HALF;
+          if (elect_one()) {
+            const uint32_t d = tmem_base + b * 256;
+            const uint64_t dx = dx0 + s * (STAGE_BYTES >> 4), dw = dw0 + s * (STAGE_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {   // 32 of the reduction each
-            const uint64_t dx = smem_desc_sw128(x_s + kk * 32, 16, 1024);
-            const uint64_t dw = W_MN ? smem_desc_sw128(w_s + kk * 4096, HALF, 1024)
-                                     : smem_desc_sw128(w_s + kk * 32, 16, 1024);
-            tc_mma_fp8_pair(tmem_base + b * 256, dx, dw, idesc, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)   // 32 of the reduction each
+              tc_mma_fp8_pair(d, dx + kk * 2, dw + kk * (W_MN ? 256 : 2), idesc, kk > 0 ? 1u : 0u);
+            tc_commit_both(bar_accf(b));
+            tc_commit_both(bar_empty(s));
           }
-          tc_commit_pair(bar_empty(s));
-          tc_commit_pair(mapa_shared(bar_empty(s), 1));
-          tc_commit_pair(bar_accf(b));
-          tc_commit_pair(mapa_shared(bar_accf(b), 1));
+          __syncwarp();
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          b ^= 1;
+          if (b == 0) aph ^= 1;
         }
       }
-      tc_commit_pair(bar_fin);
-      drain_wait(bar_fin, 0);
+      if (elect_one()) {
+        tc_commit_pair(bar_fin);
+        drain_wait(bar_fin, 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    // scales: chunks of eight reduction blocks, slot [block][128 rows, two
+    // weight blocks]; read along the blocks (32 bytes a row), written along
+    // the rows, so that an epilogue warp's scales are one shared-memory line
+    const int half = warp - 2;                  // rows [64 half, 64 half + 64)
+    const int kl = lane & 7, rl = lane >> 3;
+    int ch = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < ntiles; tile += npairs) {
+      const int row0 = (tile % p.tiles_m) * 256 + 128 * rank + 64 * half;
+      const int ob = (tile / p.tiles_m) * 2 + half;          // this warp's weight block
+      for (int k0 = 0; k0 < p.kblocks; k0 += kScaleChunk, ++ch) {
+        const uint32_t slot = ring + (ch & 1) * (kScaleChunk * kScaleStride * 4) + kl * (kScaleStride * 4);
+        ok = fp8_wait(bar_se(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag, QLORA_DEV_TIMEOUT_PRODUCER);
+        if (!warp_all(ok)) {
+          ok = false;
+          break;
+        }
+        const int kb = k0 + kl;
+        const bool live = kb < p.kblocks;
+        const float* sx = p.sx + static_cast<int64_t>(row0 + rl) * p.xblk + kb;
+#pragma unroll 1
+        for (int i = 0; i < 64; i += 32) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)     // a row or block past the end has scale zero
+            v[j] = (live && row0 + rl + i + 4 * j < p.m) ? __ldg(sx + (i + 4 * j) * p.xblk) : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sts32(slot + 4 * (64 * half + rl + i + 4 * j), __float_as_uint(v[j]));
+        }
+        if (rl == 0) {
+          const float w = (live && ob * 128 < p.cols) ? __ldg(p.sw + ob * p.sw_out + kb * p.sw_red) : 0.0f;
+          sts32(slot + 4 * (128 + half), __float_as_uint(w));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sf(ch & 1));
+      }
     }
   } else {
+    setmaxnreg_inc<kFp8PairEpiRegs>();
     const int quarter = warp & 3;               // tensor-memory lanes [32 q, 32 q + 32) belong to warp % 4
-    const int half = (warp - 2) >> 2;
+    const int cq = (warp - 4) >> 2;             // 64 of the 256 outputs
     const uint32_t acce_even0 = mapa_shared(bar_acce(0), 0);
-    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * half;
-    const uint32_t box = boxes + (warp - 2) * 8192;
-    int it = 0;
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 64 * cq;
+    const uint32_t box = boxes + (warp - 4) * 4096;
+    int it = 0, ch = 0;
     bool ok = true;
     for (int tile = pair; ok && tile < ntiles; tile += npairs) {
       const int row0 = (tile % p.tiles_m) * 256 + 128 * rank + 32 * quarter;
-      const int col0 = (tile / p.tiles_m) * 256 + 128 * half;
+      const int col0 = (tile / p.tiles_m) * 256 + 64 * cq;
       const int row = row0 + lane;
-      // a row or block past the end has no scale: its products are zero and not stored
-      const float* sx = p.sx + static_cast<int64_t>(row) * p.xblk;
-      const float* sw = p.sw + static_cast<int64_t>(col0 >> 7) * p.sw_out;
-      const bool live_x = row < p.m, live_w = col0 < p.cols;
-      float nx = live_x ? __ldg(sx) : 0.0f, nw = live_w ? __ldg(sw) : 0.0f;
-      uint64_t acc[64];
+      float acc[64];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+#pragma unroll 1
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const int b = it & 1;
-        const float s = nx * nw;
-        const uint64_t s2 = f2(s, s);
-        if (kb + 1 < p.kblocks) {
-          nx = live_x ? __ldg(sx + kb + 1) : 0.0f;
-          nw = live_w ? __ldg(sw + (kb + 1) * p.sw_red) : 0.0f;
+        const int kc = kb % kScaleChunk;
+        if (kc == 0) {
+          ok = fp8_wait(bar_sf(ch & 1), (ch >> 1) & 1, abort_flag, QLORA_DEV_TIMEOUT_EPI);
+          if (!warp_all(ok)) {
+            ok = false;
+            break;
+          }
         }
-        ok = mbar_wait(bar_accf(b), (it >> 1) & 1, abort_flag, QLORA_DEV_TIMEOUT_EPI);
+        const uint32_t slot = ring + ((ch & 1) * kScaleChunk + kc) * (kScaleStride * 4);
+        const float s = __uint_as_float(lds32(slot + 4 * (32 * quarter + lane))) *
+                        __uint_as_float(lds32(slot + 4 * (128 + (cq >> 1))));
+        if (kc == kScaleChunk - 1 || kb == p.kblocks - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_se(ch & 1));
+          ++ch;
+        }
+        ok = fp8_wait(bar_accf(b), (it >> 1) & 1, abort_flag, QLORA_DEV_TIMEOUT_EPI);
         if (!warp_all(ok)) {
           ok = false;
           break;
@@ -179,22 +243,18 @@ __global__ void __launch_bounds__(320, 1)
         const uint32_t t = tbase + b * 256;
         uint32_t ra[16], rb[16];
         tmem_ld_32x32b_x16(t, ra);
+        tmem_ld_32x32b_x16(t + 16, rb);
         tc_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          tmem_ld_32x32b_x16(t + 16 * (c + 1), rb);
-          promote16(acc + 8 * c, ra, s2);
-          tc_wait_ld();
-          if (c + 2 < 8) {
-            tmem_ld_32x32b_x16(t + 16 * (c + 2), ra);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acce_even0 + 8u * b);
-          }
-          promote16(acc + 8 * (c + 1), rb, s2);
-          if (c + 2 < 8) tc_wait_ld();
-        }
+        promote16(acc, ra, s);
+        tmem_ld_32x32b_x16(t + 32, ra);
+        promote16(acc + 16, rb, s);
+        tmem_ld_32x32b_x16(t + 48, rb);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acce_even0 + 8u * b);
+        promote16(acc + 32, ra, s);
+        promote16(acc + 48, rb, s);
       }
       if (!ok) break;
       if (p.tma_out) {
@@ -202,36 +262,27 @@ __global__ void __launch_bounds__(320, 1)
         __syncwarp();
         const uint32_t sw4 = (lane >> 1) & 3;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {          // 32 x 32 boxes in the 64-byte swizzle
+        for (int c = 0; c < 2; ++c) {          // 32 x 32 boxes in the 64-byte swizzle
           const uint32_t dst = box + c * 2048 + lane * 64;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t lo, hi;
-              f2_split(acc[16 * c + 4 * v + e], lo, hi);
-              pk[e] = pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
-            }
-            sts128(dst + ((v ^ sw4) << 4), pk[0], pk[1], pk[2], pk[3]);
+            const float* a = acc + 32 * c + 8 * v;
+            sts128(dst + ((v ^ sw4) << 4), pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                   pack_bf16x2(a[6], a[7]));
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && row0 < p.m) {
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
             if (col0 + 32 * c < p.cols) tma_store_2d(&tm_out, box + c * 2048, col0 + 32 * c, row0);
           bulk_commit();
         }
       } else if (row < p.m) {
         __nv_bfloat16* y = p.y + static_cast<int64_t>(row) * p.cols + col0;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          uint32_t lo, hi;
-          f2_split(acc[i], lo, hi);
-          if (col0 + 2 * i < p.cols) y[2 * i] = __float2bfloat16_rn(__uint_as_float(lo));
-          if (col0 + 2 * i + 1 < p.cols) y[2 * i + 1] = __float2bfloat16_rn(__uint_as_float(hi));
-        }
+        for (int i = 0; i < 64; ++i)
+          if (col0 + i < p.cols) y[i] = __float2bfloat16_rn(acc[i]);
       }
     }
     if (lane == 0) bulk_wait_all();   // stores complete before the CTA's shared memory goes away
