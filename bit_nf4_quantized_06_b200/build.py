@@ -22,7 +22,10 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(HERE, "libqlora.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+RDC = ["-rdc=true"]
+# ptxas ignores setmaxnreg in relocatable device code: these files share no device symbols with the others
+STANDALONE = {"fp8_pair.cu"}
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
 
 
@@ -51,7 +54,8 @@ def up_to_date():
 
 def _compile(nvcc, src, extra, verbose):
     obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc] + ARCH + FLAGS + extra + ["-c", src, "-o", obj]
+    rdc = [] if os.path.basename(src) in STANDALONE else RDC
+    cmd = [nvcc] + ARCH + FLAGS + rdc + extra + ["-c", src, "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -100,6 +100,7 @@ struct DevState {
   bool attrs = false;      // kernel attributes set in context `ctx`
   CUcontext ctx = nullptr;
   int pair_clusters = 0;   // CTA pairs of k_tc_pair that can be resident at once
+  unsigned int* status = nullptr;   // g_dev_status in context `ctx`
 };
 std::mutex g_mu;
 DevState g_dev[64];
@@ -228,6 +229,7 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
       e = cudaFuncSetAttribute(k_merge_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(merge_tc_smem_bytes()));
     if (e == cudaSuccess) e = set_fp8_attributes();
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&st.status), g_dev_status);
     if (e != cudaSuccess) return QLORA_ERR_CUDA;
     st.attrs = true;
     st.ctx = ctx;
@@ -242,6 +244,12 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
 // The same device check every entry point runs first (see device_ready), for
 // the entry points defined in other files.
 int check_current_device_status() { return static_cast<int>(device_ready(nullptr)); }
+unsigned int* device_status_word() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lk(g_mu);
+  return g_dev[dev].status;
+}
 int check_current_device(int* sms, int* pairs) { return static_cast<int>(device_ready(sms, pairs)); }
 
 namespace {

@@ -11,7 +11,7 @@
 
 #include "../../include/qlora.h"
 #include "fp8_dev.cuh"
-#include "fp8_pair.h"
+#include "fp8_launch.h"
 #include "host.h"
 #include "ptx.cuh"
 
@@ -182,6 +182,7 @@ qlora_status_t check_weight(const qlora_fp8_t* q) {
 template <bool BWD>
 int launch_pair_product(const Product& p, int format, int pairs, cudaStream_t st) {
   Fp8Gemm g{};
+  g.status = device_status_word();
   g.sx = p.sx;
   g.sw = p.sw;
   g.y = p.y;
@@ -203,9 +204,7 @@ int launch_pair_product(const Product& p, int format, int pairs, cudaStream_t st
       (g.tma_out && !encode_map2d(&o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.y, p.cols, p.m, p.cols * 2, 32, 32,
                                   CU_TENSOR_MAP_SWIZZLE_64B)))
     return QLORA_ERR_CUDA;
-  const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
-  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
-  return host::launch_pdl(k_fp8_pair<BWD>, dim3(grid), dim3(kFp8PairThreads), kFp8PairSmem, st, 2, x, w, o, g);
+  return launch_fp8_pair(BWD, x, w, o, g, pairs, st);
 }
 
 // Workspace of a product over rows of `red` values: the rows' codes and scales.
@@ -260,12 +259,7 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
 
 }  // namespace
 
-cudaError_t set_fp8_attributes() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_fp8_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFp8PairSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_fp8_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFp8PairSmem);
-}
+cudaError_t set_fp8_attributes() { return set_fp8_pair_attributes(); }
 
 }  // namespace qlora
 

@@ -1,43 +1,41 @@
 // Tensor-core product of 8-bit rows with an 8-bit weight: parameters and
-// helpers shared by the CTA-pair kernel and the split kernel.
+// device helpers. For files compiled without relocatable device code, under
+// which ptxas ignores setmaxnreg.
 #pragma once
+
+#define QLORA_STANDALONE
 
 #include <cuda_bf16.h>
 
 #include "fp8_dev.cuh"
+#include "fp8_launch.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
 namespace qlora {
 
-struct Fp8Gemm {
-  const float* sx;          // [m x xblk] scales of the rows
-  const float* sw;          // scales of the weight, at output block * sw_out + reduction block * sw_red
-  __nv_bfloat16* y;         // [m x cols]
-  int64_t xblk, sw_out, sw_red;
-  int32_t m, cols;
-  int32_t kblocks;          // reduction blocks of 128
-  int32_t tiles_m, tiles_n;
-  int32_t a_format;         // format of the rows' codes (Fp8Format)
-  int32_t tma_out;          // output through TMA stores (cols % 8 == 0)
+// Bounded wait for the phase with the given parity: plain tries first (the
+// timer of the bound is slow to read next to a step of this pipeline), then
+// tries under the library's time limit. On timeout, or when another role has
+// given up, false; a timeout sets `code` in the device status word.
+struct Fp8Abort {
+  volatile int* flag;       // shared memory, one a CTA
+  unsigned int* status;     // the library's device status word
 };
-
-// The bounded waits of ptx.cuh after a number of plain tries: the timer of
-// the bound is slow to read next to a step of this pipeline (512 cycles), and
-// most waits end within a few tries.
-constexpr int kPlainTries = 256;
-__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
 #pragma unroll 1
-  for (int i = 0; i < kPlainTries; ++i)
+  for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort_flag, code);
-}
-__device__ __forceinline__ bool fp8_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                 unsigned code) {
-#pragma unroll 1
-  for (int i = 0; i < kPlainTries; ++i)
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-  return mbar_wait_cluster(bar, parity, abort_flag, code);
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*a.flag) return false;
+    if (globaltimer_ns() - t0 > QLORA_WAIT_LIMIT_NS) {
+      atomicOr(a.status, code);
+      *a.flag = 1;
+      return false;
+    }
+  }
 }
 
 // Instruction descriptor for kind::f8f6f4: A e4m3 or e5m2, B e4m3, fp32 D.
@@ -100,11 +98,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// acc[i] += t[i] * s. Plain FMAs: packed in pairs they took a register move a
-// value on the way.
-__device__ __forceinline__ void promote16(float* acc, const uint32_t (&t)[16], float s) {
+// acc[i] += t[2i, 2i+1] * s, in pairs
+__device__ __forceinline__ void promote16(uint64_t* acc, const uint32_t (&t)[16], uint64_t s2) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = fmaf(__uint_as_float(t[i]), s, acc[i]);
+  for (int i = 0; i < 8; ++i) acc[i] = f2_fma(f2(__uint_as_float(t[2 * i]), __uint_as_float(t[2 * i + 1])), s2, acc[i]);
 }
 
 }  // namespace qlora

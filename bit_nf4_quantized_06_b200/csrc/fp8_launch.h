@@ -1,0 +1,33 @@
+// Parameters and launches of the 8-bit product's tensor-core kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace qlora {
+
+struct Fp8Gemm {
+  unsigned int* status;     // the library's device status word
+  const float* sx;          // [m x xblk] scales of the rows
+  const float* sw;          // scales of the weight, at output block * sw_out + reduction block * sw_red
+  __nv_bfloat16* y;         // [m x cols]
+  int64_t xblk, sw_out, sw_red;
+  int32_t m, cols;
+  int32_t kblocks;          // reduction blocks of 128
+  int32_t tiles_m, tiles_n;
+  int32_t a_format;         // format of the rows' codes (Fp8Format)
+  int32_t tma_out;          // output through TMA stores (cols % 8 == 0)
+};
+
+// CTA-pair kernel (fp8_pair.cu). tm_x: rows' codes [m x red], boxes
+// {128, 128}; tm_w: weight codes [N x K], boxes {128, 128}, both 128-byte
+// swizzled; tm_out: y [m x cols] bf16, boxes {32, 32}, 64-byte swizzled
+// (p.tma_out). `w_mn`: the reduction runs along N (dX).
+int launch_fp8_pair(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_out,
+                    const Fp8Gemm& p, int pairs, cudaStream_t st);
+cudaError_t set_fp8_pair_attributes();
+
+}  // namespace qlora

@@ -24,11 +24,28 @@
 // Warps of a CTA (320 threads): 0 TMA; 1 tensor-memory allocation and, in the
 // even CTA, the MMA issue; 2-9 epilogue (lane quarter = warp % 4, output half
 // = (warp - 2) / 4). Every wait is bounded.
-#include "fp8_pair.h"
+#include <algorithm>
+
+#include "fp8_gemm.cuh"
+#include "host.h"
 
 namespace qlora {
+namespace {
 
 using namespace tcd;
+
+constexpr int kFp8PairStages = 4;            // 32 KB each
+constexpr int kFp8PairThreads = 384;         // TMA, MMA and two scale warps; 8 epilogue warps
+constexpr int kFp8PairIssueRegs = 56, kFp8PairEpiRegs = 216;
+// 384 threads are launched with at most 168 registers each
+static_assert(128 * kFp8PairIssueRegs + 256 * kFp8PairEpiRegs <= 384 * 168, "registers of the launch");
+constexpr int kFp8PairBoxes = 8 * 4 * 2048;  // four 32 x 32 bf16 output boxes an epilogue warp
+// scales: two chunks of eight reduction blocks, each block 128 rows' and two
+// weight blocks' (132 words: a warp's transposed stores spread over the banks)
+constexpr int kScaleChunk = 8, kScaleStride = 132;
+constexpr int kFp8PairRing = 2 * kScaleChunk * kScaleStride * 4;
+constexpr int kFp8PairSmem = kFp8PairStages * 32768 + kFp8PairBoxes + kFp8PairRing + 1024 + 256;
+
 
 template <bool W_MN>
 __global__ void __launch_bounds__(kFp8PairThreads, 1)
@@ -47,12 +64,13 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
   auto bar_full = [&](int s) { return bar0 + 8u * s; };                  // even CTA: loads of both
   auto bar_empty = [&](int s) { return bar0 + 8u * (STAGES + s); };      // local, from the MMA
   auto bar_accf = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };   // local, from the MMA
-  auto bar_acce = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };   // even CTA: 32 epilogue warps
+  auto bar_acce = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };   // even CTA: 16 epilogue warps
   auto bar_sf = [&](int c) { return bar0 + 8u * (2 * STAGES + 4 + c); };     // two scale warps
-  auto bar_se = [&](int c) { return bar0 + 8u * (2 * STAGES + 6 + c); };     // 16 epilogue warps
+  auto bar_se = [&](int c) { return bar0 + 8u * (2 * STAGES + 6 + c); };     // 8 epilogue warps
   const uint32_t bar_fin = bar0 + 8u * (2 * STAGES + 8);
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(ctl + 8 * (2 * STAGES + 9));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * (2 * STAGES + 9) + 4);
+  const Fp8Abort ab{abort_flag, p.status};
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -69,9 +87,9 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_accf(b), 1);
-      mbar_init(bar_acce(b), 32);
+      mbar_init(bar_acce(b), 16);
       mbar_init(bar_sf(b), 2);
-      mbar_init(bar_se(b), 16);
+      mbar_init(bar_se(b), 8);
     }
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
@@ -102,7 +120,7 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
         const int out = (tile / p.tiles_m) * 256 + 128 * rank;
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const int s = it % STAGES;
-          if (!fp8_wait(bar_empty(s), ((it / STAGES) & 1) ^ 1, abort_flag, QLORA_DEV_TIMEOUT_PRODUCER)) {
+          if (!fp8_wait(bar_empty(s), ((it / STAGES) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER)) {
             ok = false;
             break;
           }
@@ -131,8 +149,8 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       bool ok = true;
       for (int tile = pair; ok && tile < ntiles; tile += npairs) {
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!fp8_wait(bar_acce(b), aph, abort_flag, QLORA_DEV_TIMEOUT_MMA) ||
-              !fp8_wait(bar_full(s), ph, abort_flag, QLORA_DEV_TIMEOUT_MMA)) {
+          if (!fp8_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA) ||
+              !fp8_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
@@ -174,7 +192,7 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       const int ob = (tile / p.tiles_m) * 2 + half;          // this warp's weight block
       for (int k0 = 0; k0 < p.kblocks; k0 += kScaleChunk, ++ch) {
         const uint32_t slot = ring + (ch & 1) * (kScaleChunk * kScaleStride * 4) + kl * (kScaleStride * 4);
-        ok = fp8_wait(bar_se(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag, QLORA_DEV_TIMEOUT_PRODUCER);
+        ok = fp8_wait(bar_se(ch & 1), ((ch >> 1) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER);
         if (!warp_all(ok)) {
           ok = false;
           break;
@@ -202,39 +220,43 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
   } else {
     setmaxnreg_inc<kFp8PairEpiRegs>();
     const int quarter = warp & 3;               // tensor-memory lanes [32 q, 32 q + 32) belong to warp % 4
-    const int cq = (warp - 4) >> 2;             // 64 of the 256 outputs
+    const int half = (warp - 4) >> 2;           // 128 of the 256 outputs: one weight block
     const uint32_t acce_even0 = mapa_shared(bar_acce(0), 0);
-    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 64 * cq;
-    const uint32_t box = boxes + (warp - 4) * 4096;
-    int it = 0, ch = 0;
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * half;
+    const uint32_t box = boxes + (warp - 4) * 8192;
+    const uint32_t ring_x = ring + 4 * (32 * quarter + lane), ring_w = ring + 4 * (128 + half);
+    int b = 0, c = 0;              // accumulator buffer, scale chunk buffer
+    uint32_t bph = 0, cph = 0;     // their parities
     bool ok = true;
     for (int tile = pair; ok && tile < ntiles; tile += npairs) {
       const int row0 = (tile % p.tiles_m) * 256 + 128 * rank + 32 * quarter;
-      const int col0 = (tile / p.tiles_m) * 256 + 64 * cq;
-      const int row = row0 + lane;
-      float acc[64];
+      const int col0 = (tile / p.tiles_m) * 256 + 128 * half;
+      uint64_t acc[64];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      int left = 0;                // blocks left in the scale chunk
+      uint32_t slot = 0;
 #pragma unroll 1
-      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-        const int b = it & 1;
-        const int kc = kb % kScaleChunk;
-        if (kc == 0) {
-          ok = fp8_wait(bar_sf(ch & 1), (ch >> 1) & 1, abort_flag, QLORA_DEV_TIMEOUT_EPI);
+      for (int kb = p.kblocks; kb > 0; --kb) {
+        if (left == 0) {
+          ok = fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
           if (!warp_all(ok)) {
             ok = false;
             break;
           }
+          left = min(kb, kScaleChunk);
+          slot = c * (kScaleChunk * kScaleStride * 4);
         }
-        const uint32_t slot = ring + ((ch & 1) * kScaleChunk + kc) * (kScaleStride * 4);
-        const float s = __uint_as_float(lds32(slot + 4 * (32 * quarter + lane))) *
-                        __uint_as_float(lds32(slot + 4 * (128 + (cq >> 1))));
-        if (kc == kScaleChunk - 1 || kb == p.kblocks - 1) {
+        const float s = __uint_as_float(lds32(ring_x + slot)) * __uint_as_float(lds32(ring_w + slot));
+        const uint64_t s2 = f2(s, s);
+        slot += kScaleStride * 4;
+        if (--left == 0) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_se(ch & 1));
-          ++ch;
+          if (lane == 0) mbar_arrive(bar_se(c));
+          c ^= 1;
+          if (c == 0) cph ^= 1;
         }
-        ok = fp8_wait(bar_accf(b), (it >> 1) & 1, abort_flag, QLORA_DEV_TIMEOUT_EPI);
+        ok = fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
         if (!warp_all(ok)) {
           ok = false;
           break;
@@ -244,17 +266,21 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
         uint32_t ra[16], rb[16];
         tmem_ld_32x32b_x16(t, ra);
         tmem_ld_32x32b_x16(t + 16, rb);
-        tc_wait_ld();
-        promote16(acc, ra, s);
-        tmem_ld_32x32b_x16(t + 32, ra);
-        promote16(acc + 16, rb, s);
-        tmem_ld_32x32b_x16(t + 48, rb);
-        tc_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acce_even0 + 8u * b);
-        promote16(acc + 32, ra, s);
-        promote16(acc + 48, rb, s);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          tc_wait_ld();
+          if (i == 6) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acce_even0 + 8u * b);
+          }
+          promote16(acc + 8 * i, ra, s2);
+          if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 2), ra);
+          promote16(acc + 8 * (i + 1), rb, s2);
+          if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 3), rb);
+        }
+        b ^= 1;
+        if (b == 0) bph ^= 1;
       }
       if (!ok) break;
       if (p.tma_out) {
@@ -262,27 +288,36 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
         __syncwarp();
         const uint32_t sw4 = (lane >> 1) & 3;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {          // 32 x 32 boxes in the 64-byte swizzle
-          const uint32_t dst = box + c * 2048 + lane * 64;
+        for (int c4 = 0; c4 < 4; ++c4) {       // 32 x 32 boxes in the 64-byte swizzle
+          const uint32_t dst = box + c4 * 2048 + lane * 64;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const float* a = acc + 32 * c + 8 * v;
-            sts128(dst + ((v ^ sw4) << 4), pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                   pack_bf16x2(a[6], a[7]));
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t lo, hi;
+              f2_split(acc[16 * c4 + 4 * v + e], lo, hi);
+              pk[e] = pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+            }
+            sts128(dst + ((v ^ sw4) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && row0 < p.m) {
-          for (int c = 0; c < 2; ++c)
-            if (col0 + 32 * c < p.cols) tma_store_2d(&tm_out, box + c * 2048, col0 + 32 * c, row0);
+          for (int c4 = 0; c4 < 4; ++c4)
+            if (col0 + 32 * c4 < p.cols) tma_store_2d(&tm_out, box + c4 * 2048, col0 + 32 * c4, row0);
           bulk_commit();
         }
-      } else if (row < p.m) {
-        __nv_bfloat16* y = p.y + static_cast<int64_t>(row) * p.cols + col0;
+      } else if (row0 + lane < p.m) {
+        __nv_bfloat16* y = p.y + static_cast<int64_t>(row0 + lane) * p.cols + col0;
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (col0 + i < p.cols) y[i] = __float2bfloat16_rn(acc[i]);
+        for (int i = 0; i < 64; ++i) {
+          uint32_t lo, hi;
+          f2_split(acc[i], lo, hi);
+          if (col0 + 2 * i < p.cols) y[2 * i] = __float2bfloat16_rn(__uint_as_float(lo));
+          if (col0 + 2 * i + 1 < p.cols) y[2 * i + 1] = __float2bfloat16_rn(__uint_as_float(hi));
+        }
       }
     }
     if (lane == 0) bulk_wait_all();   // stores complete before the CTA's shared memory goes away
@@ -297,9 +332,26 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
   }
 }
 
-template __global__ void k_fp8_pair<false>(const __grid_constant__ CUtensorMap, const __grid_constant__ CUtensorMap,
-                                           const __grid_constant__ CUtensorMap, Fp8Gemm);
-template __global__ void k_fp8_pair<true>(const __grid_constant__ CUtensorMap, const __grid_constant__ CUtensorMap,
-                                          const __grid_constant__ CUtensorMap, Fp8Gemm);
+template <bool W_MN>
+int launch(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& o, const Fp8Gemm& p, int pairs,
+           cudaStream_t st) {
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
+  return host::launch_pdl(k_fp8_pair<W_MN>, dim3(grid), dim3(kFp8PairThreads), kFp8PairSmem, st, 2, x, w, o, p);
+}
+
+}  // namespace
+
+int launch_fp8_pair(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_out,
+                    const Fp8Gemm& p, int pairs, cudaStream_t st) {
+  return w_mn ? launch<true>(tm_x, tm_w, tm_out, p, pairs, st) : launch<false>(tm_x, tm_w, tm_out, p, pairs, st);
+}
+
+cudaError_t set_fp8_pair_attributes() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_fp8_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFp8PairSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_fp8_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFp8PairSmem);
+}
 
 }  // namespace qlora

@@ -17,6 +17,10 @@ int check_current_device(int* sms, int* pairs = nullptr);
 // device check, which sets every kernel's attributes once a context.
 cudaError_t set_fp8_attributes();
 
+// Device address of the status word (ptx.cuh) on the current device, after a
+// successful device check.
+unsigned int* device_status_word();
+
 // Counts a launch and returns its status (a qlora_status_t).
 int launch_done();
 

@@ -24,7 +24,12 @@
 
 namespace qlora {
 
+// Files compiled on their own (without relocatable device code) cannot see
+// the status word; they define QLORA_STANDALONE, get its address as a kernel
+// argument and bring their own waits.
+#ifndef QLORA_STANDALONE
 extern __device__ unsigned int g_dev_status;
+#endif
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
@@ -66,6 +71,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+#ifndef QLORA_STANDALONE
 // Bounded wait for the phase with the given parity to complete. On timeout
 // (or when another role already aborted) records `code` and returns false.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
@@ -83,6 +89,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+#endif
+
 // ------------------------------------------------------------------ global flags
 __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {
   uint32_t v;
@@ -94,6 +102,7 @@ __device__ __forceinline__ void st_release_gpu(uint32_t* p, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+#ifndef QLORA_STANDALONE
 // Bounded wait until *flag != 0 (acquire at GPU scope); on timeout (or when
 // another role already aborted) records `code` and returns false.
 __device__ __forceinline__ bool flag_wait(const uint32_t* flag, volatile int* abort_flag, unsigned code) {
@@ -110,6 +119,8 @@ __device__ __forceinline__ bool flag_wait(const uint32_t* flag, volatile int* ab
     __nanosleep(100);
   }
 }
+
+#endif
 
 // ------------------------------------------------------------------ fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -254,6 +265,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+#ifndef QLORA_STANDALONE
 // Bounded wait with cluster-scope acquire (for barriers other CTAs arrive on).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   unsigned code) {
@@ -269,6 +281,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
   }
 }
+
+#endif
 
 // 2D tiled TMA load into this CTA's shared memory whose completion is counted
 // on an mbarrier of either CTA of the pair (cluster address). The data goes
