@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libqlora.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 RDC = ["-rdc=true"]
 # ptxas ignores setmaxnreg in relocatable device code: these files share no device symbols with the others
-STANDALONE = {"fp8_pair.cu"}
+STANDALONE = {"fp8_pair.cu", "fp8_split.cu"}
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
 

@@ -98,71 +98,6 @@ __global__ void __launch_bounds__(256) k_dequantize_fp8(const uint8_t* __restric
   }
 }
 
-// ------------------------------------------------------------------ product
-struct Product {
-  const uint8_t* x;        // [m x red] codes, ldx bytes from row to row
-  const float* sx;         // [m x xblk]
-  const uint8_t* w;        // weight codes [N x K]
-  const float* sw;         // [ceil(N/128) x nbk]
-  __nv_bfloat16* y;        // [m x cols]
-  int64_t m, cols, red;    // red: K forward, N backward
-  int64_t ldx, xblk, k, nbk;
-};
-
-// 64 x 64 outputs a CTA, 16 a thread, the reduction in steps of 32.
-template <bool BWD, int FMT>
-__global__ void __launch_bounds__(256) k_fp8_product(Product p) {
-  __shared__ float sx[32][65], sw[32][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
-  float acc[4][4] = {}, part[4][4] = {};
-  grid_dependency_wait();
-  grid_dependency_trigger();
-  for (int64_t r0 = 0; r0 < p.red; r0 += 32) {
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-      const int a = i >> 5, r = i & 31;
-      sx[r][a] = (m0 + a < p.m && r0 + r < p.red) ? fp8_unpack2<FMT>(p.x[(m0 + a) * p.ldx + r0 + r]).x : 0.0f;
-      if (!BWD)
-        sw[r][a] = (c0 + a < p.cols && r0 + r < p.red) ? fp8_unpack2<kE4M3>(p.w[(c0 + a) * p.k + r0 + r]).x : 0.0f;
-    }
-    if (BWD)
-      for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-        const int a = i & 63, r = i >> 6;
-        sw[r][a] = (c0 + a < p.cols && r0 + r < p.red) ? fp8_unpack2<kE4M3>(p.w[(r0 + r) * p.k + c0 + a]).x : 0.0f;
-      }
-    __syncthreads();
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sx[r][ty + 16 * i], sw[r][tx + 16 * j], part[i][j]);
-    __syncthreads();
-    if ((r0 + 32) % kFp8Block == 0 || r0 + 32 >= p.red) {
-      const int64_t b = r0 / kFp8Block;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t m = m0 + ty + 16 * i, c = c0 + tx + 16 * j;
-          if (m < p.m && c < p.cols) {
-            const int64_t cb = c / kFp8Block;
-            const float s = p.sx[m * p.xblk + b] * p.sw[BWD ? b * p.nbk + cb : cb * p.nbk + b];
-            acc[i][j] = fmaf(part[i][j], s, acc[i][j]);
-          }
-          part[i][j] = 0.0f;
-        }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, c = c0 + tx + 16 * j;
-      if (m < p.m && c < p.cols) p.y[m * p.cols + c] = __float2bfloat16_rn(acc[i][j]);
-    }
-}
-
 // ------------------------------------------------------------------ host
 using host::al256;
 using host::aligned;
@@ -179,30 +114,73 @@ qlora_status_t check_weight(const qlora_fp8_t* q) {
   return QLORA_OK;
 }
 
+struct Product {
+  qlora_fp8_rows_t x;      // [m x red]
+  const qlora_fp8_t* q;
+  void* y;                 // [m x cols]
+  int64_t m, cols, red;    // red: K forward, N backward
+  bool quantized_here;     // the rows' quantizer is the kernel in front
+};
+
+// The tile shape and the split, by an estimate of the time in reduction blocks
+// of 128 (unit: one block of the pair kernel's 256 x 256 tile).
+struct Choice {
+  bool pair;
+  int splits;
+};
+
+Choice choose(int64_t m, int64_t cols, int64_t kblocks, int sms, int pairs) {
+  const int64_t pair_waves = cdiv(cdiv(m, 256) * cdiv(cols, 256), pairs);
+  const double pair_cost = static_cast<double>(pair_waves) * (kblocks + 6.0);
+  const int64_t tiles = cdiv(m, 128) * cdiv(cols, 128);
+  Choice best{true, 1};
+  double best_cost = pair_cost;
+  for (int s = 1; s <= 8 && s <= kblocks && tiles * s < (int64_t(1) << 30); ++s) {
+    const int64_t waves = cdiv(tiles * s, sms);
+    const double cost = static_cast<double>(waves) * (0.45 * static_cast<double>(cdiv(kblocks, s)) + 3.0 + 0.3 * s);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = Choice{false, s};
+    }
+  }
+  return best;
+}
+
 template <bool BWD>
-int launch_pair_product(const Product& p, int format, int pairs, cudaStream_t st) {
+int launch_product(const Product& p, int sms, int pairs, cudaStream_t st) {
+  const qlora_fp8_t& q = *p.q;
+  const int64_t nbk = cdiv(q.k_in, kFp8Block);
   Fp8Gemm g{};
   g.status = device_status_word();
-  g.sx = p.sx;
-  g.sw = p.sw;
-  g.y = p.y;
-  g.xblk = p.xblk;
-  g.sw_out = BWD ? 1 : p.nbk;
-  g.sw_red = BWD ? p.nbk : 1;
+  g.sx = p.x.scales;
+  g.sw = q.scales;
+  g.y = static_cast<__nv_bfloat16*>(p.y);
+  g.xblk = cdiv(p.red, kFp8Block);
+  g.sw_out = BWD ? 1 : nbk;
+  g.sw_red = BWD ? nbk : 1;
   g.m = static_cast<int32_t>(p.m);
   g.cols = static_cast<int32_t>(p.cols);
-  g.kblocks = static_cast<int32_t>(p.xblk);
-  g.tiles_m = static_cast<int32_t>(cdiv(p.m, 256));
-  g.tiles_n = static_cast<int32_t>(cdiv(p.cols, 256));
-  g.a_format = format;
+  g.kblocks = static_cast<int32_t>(g.xblk);
+  g.a_format = p.x.format;
   g.tma_out = p.cols % 8 == 0;
+  if (cdiv(p.m, 256) * cdiv(p.cols, 256) > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;   // tile numbers are 32-bit
+  const Choice c = choose(p.m, p.cols, g.xblk, sms, pairs);
+  const int tile = c.pair ? 256 : 128;
+  g.tiles_m = static_cast<int32_t>(cdiv(p.m, tile));
+  g.tiles_n = static_cast<int32_t>(cdiv(p.cols, tile));
+  g.splits = c.splits;
+  g.box_m = c.pair ? 128 : static_cast<int32_t>(std::min<int64_t>(128, rup(p.m, 8)));
+  g.early_w = p.quantized_here;
   CUtensorMap x, w, o;
   std::memset(&o, 0, sizeof(o));
-  const int64_t n = BWD ? p.red : p.cols;
-  if (!encode_map2d(&x, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x, p.red, p.m, p.ldx, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.k, n, p.k, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (g.tma_out && !encode_map2d(&o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.y, p.cols, p.m, p.cols * 2, 32, 32,
-                                  CU_TENSOR_MAP_SWIZZLE_64B)))
+  if (!encode_map2d(&x, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x.codes, p.red, p.m, p.x.ld, 128, g.box_m,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, q.k_in, q.n_out, q.k_in, 128, 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  if (!c.pair) return launch_fp8_split(BWD, x, w, g, st);
+  if (g.tma_out && !encode_map2d(&o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.y, p.cols, p.m, p.cols * 2, 32, 32,
+                                 CU_TENSOR_MAP_SWIZZLE_64B))
     return QLORA_ERR_CUDA;
   return launch_fp8_pair(BWD, x, w, o, g, pairs, st);
 }
@@ -248,18 +226,16 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
                             format, 0};
     if ((s = static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, rows, st))) != QLORA_OK) return s;
   }
-  Product p{rows.codes, rows.scales, q->codes, q->scales, static_cast<__nv_bfloat16*>(out_bf16), m, cols, red,
-            rows.ld, cdiv(red, kFp8Block), q->k_in, cdiv(q->k_in, kFp8Block)};
-  if (m > 128) return static_cast<qlora_status_t>(launch_pair_product<BWD>(p, rows.format, pairs, st));
-  const dim3 grid(static_cast<unsigned>(cdiv(cols, 64)), static_cast<unsigned>(cdiv(m, 64)));
-  return static_cast<qlora_status_t>(
-      rows.format == QLORA_FP8_E5M2 ? host::launch_pdl(k_fp8_product<BWD, kE5M2>, grid, dim3(256), 0, st, 1, p)
-                                    : host::launch_pdl(k_fp8_product<BWD, kE4M3>, grid, dim3(256), 0, st, 1, p));
+  const Product p{rows, q, out_bf16, m, cols, red, x8 == nullptr};
+  return static_cast<qlora_status_t>(launch_product<BWD>(p, sms, pairs, st));
 }
 
 }  // namespace
 
-cudaError_t set_fp8_attributes() { return set_fp8_pair_attributes(); }
+cudaError_t set_fp8_attributes() {
+  const cudaError_t e = set_fp8_pair_attributes();
+  return e == cudaSuccess ? set_fp8_split_attributes() : e;
+}
 
 }  // namespace qlora
 

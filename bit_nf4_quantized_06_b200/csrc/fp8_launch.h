@@ -19,7 +19,11 @@ struct Fp8Gemm {
   int32_t kblocks;          // reduction blocks of 128
   int32_t tiles_m, tiles_n;
   int32_t a_format;         // format of the rows' codes (Fp8Format)
-  int32_t tma_out;          // output through TMA stores (cols % 8 == 0)
+  int32_t tma_out;          // output rows are 16-byte aligned (cols % 8 == 0)
+  // split kernel
+  int32_t splits;           // CTAs of a cluster that share a tile's reduction
+  int32_t box_m;            // rows of tm_x's boxes
+  int32_t early_w;          // the kernel in front has waited for everything before it
 };
 
 // CTA-pair kernel (fp8_pair.cu). tm_x: rows' codes [m x red], boxes
@@ -29,5 +33,11 @@ struct Fp8Gemm {
 int launch_fp8_pair(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_out,
                     const Fp8Gemm& p, int pairs, cudaStream_t st);
 cudaError_t set_fp8_pair_attributes();
+
+// Split kernel (fp8_split.cu): 128 x 128 tiles, the reduction over clusters
+// of p.splits (1 to 8, at most the number of blocks). tm_x: boxes {128,
+// p.box_m}; tm_w: boxes {128, 128}.
+int launch_fp8_split(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8Gemm& p, cudaStream_t st);
+cudaError_t set_fp8_split_attributes();
 
 }  // namespace qlora
