@@ -122,22 +122,31 @@ struct Product {
   bool quantized_here;     // the rows' quantizer is the kernel in front
 };
 
-// The tile shape and the split, by an estimate of the time in reduction blocks
-// of 128 (unit: one block of the pair kernel's 256 x 256 tile).
+// The tile shape and the split, by an estimate of the time in microseconds.
+// Measured on B200 with rows already in 8 bits:
+//   pair kernel   5 + waves (1.5 + 0.55 blocks): 4096^3 70.7, 512 rows x 4096 x 4096 19.6
+//   split kernel  waves (4.6 + S (0.1 + 0.002 rows) + 0.32 ceil(blocks / S)), a wave being the
+//                 clusters of S CTAs that are resident at once:
+//                 4096 x 4096 weight, 1 row: 12.6 (S = 1), 8.0 (2), 6.4 (4), 14.4 (8, two waves);
+//                 128 rows: 14.6, 10.4, 9.0, 23.1; 512 rows, S = 1: 15.2 (pair 19.6); 1024 rows: 30.5 (pair 20.7)
 struct Choice {
   bool pair;
   int splits;
 };
 
-Choice choose(int64_t m, int64_t cols, int64_t kblocks, int sms, int pairs) {
+Choice choose(int64_t m, int64_t cols, int64_t kblocks, int dev, int pairs) {
+  const double blocks = static_cast<double>(kblocks);
   const int64_t pair_waves = cdiv(cdiv(m, 256) * cdiv(cols, 256), pairs);
-  const double pair_cost = static_cast<double>(pair_waves) * (kblocks + 6.0);
-  const int64_t tiles = cdiv(m, 128) * cdiv(cols, 128);
   Choice best{true, 1};
-  double best_cost = pair_cost;
-  for (int s = 1; s <= 8 && s <= kblocks && tiles * s < (int64_t(1) << 30); ++s) {
-    const int64_t waves = cdiv(tiles * s, sms);
-    const double cost = static_cast<double>(waves) * (0.45 * static_cast<double>(cdiv(kblocks, s)) + 3.0 + 0.3 * s);
+  double best_cost = 5.0 + static_cast<double>(pair_waves) * (1.5 + 0.55 * blocks);
+  const int64_t tiles = cdiv(m, 128) * cdiv(cols, 128);
+  const double rows = static_cast<double>(std::min<int64_t>(m, 128));
+  for (int s = 1; s <= kFp8MaxSplits && s <= kblocks && tiles * s < (int64_t(1) << 30); ++s) {
+    const int resident = fp8_split_clusters(dev, s);
+    if (resident < 1) continue;
+    const double waves = static_cast<double>(cdiv(tiles, resident));
+    const double cost =
+        waves * (4.6 + (s > 1 ? s * (0.1 + 0.002 * rows) : 0.0) + 0.32 * static_cast<double>(cdiv(kblocks, s)));
     if (cost < best_cost) {
       best_cost = cost;
       best = Choice{false, s};
@@ -147,7 +156,9 @@ Choice choose(int64_t m, int64_t cols, int64_t kblocks, int sms, int pairs) {
 }
 
 template <bool BWD>
-int launch_product(const Product& p, int sms, int pairs, cudaStream_t st) {
+int launch_product(const Product& p, int pairs, cudaStream_t st) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_CUDA;
   const qlora_fp8_t& q = *p.q;
   const int64_t nbk = cdiv(q.k_in, kFp8Block);
   Fp8Gemm g{};
@@ -164,7 +175,7 @@ int launch_product(const Product& p, int sms, int pairs, cudaStream_t st) {
   g.a_format = p.x.format;
   g.tma_out = p.cols % 8 == 0;
   if (cdiv(p.m, 256) * cdiv(p.cols, 256) > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;   // tile numbers are 32-bit
-  const Choice c = choose(p.m, p.cols, g.xblk, sms, pairs);
+  const Choice c = choose(p.m, p.cols, g.xblk, dev, pairs);
   const int tile = c.pair ? 256 : 128;
   g.tiles_m = static_cast<int32_t>(cdiv(p.m, tile));
   g.tiles_n = static_cast<int32_t>(cdiv(p.cols, tile));
@@ -227,14 +238,14 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
     if ((s = static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, rows, st))) != QLORA_OK) return s;
   }
   const Product p{rows, q, out_bf16, m, cols, red, x8 == nullptr};
-  return static_cast<qlora_status_t>(launch_product<BWD>(p, sms, pairs, st));
+  return static_cast<qlora_status_t>(launch_product<BWD>(p, pairs, st));
 }
 
 }  // namespace
 
-cudaError_t set_fp8_attributes() {
+cudaError_t set_fp8_attributes(int dev) {
   const cudaError_t e = set_fp8_pair_attributes();
-  return e == cudaSuccess ? set_fp8_split_attributes() : e;
+  return e == cudaSuccess ? set_fp8_split_attributes(dev) : e;
 }
 
 }  // namespace qlora

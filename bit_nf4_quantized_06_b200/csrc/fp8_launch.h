@@ -35,9 +35,12 @@ int launch_fp8_pair(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
 cudaError_t set_fp8_pair_attributes();
 
 // Split kernel (fp8_split.cu): 128 x 128 tiles, the reduction over clusters
-// of p.splits (1 to 8, at most the number of blocks). tm_x: boxes {128,
+// of p.splits (1 to kFp8MaxSplits, at most the number of blocks). tm_x: boxes {128,
 // p.box_m}; tm_w: boxes {128, 128}.
 int launch_fp8_split(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8Gemm& p, cudaStream_t st);
-cudaError_t set_fp8_split_attributes();
+cudaError_t set_fp8_split_attributes(int dev);
+constexpr int kFp8MaxSplits = 8;
+// How many clusters of `splits` CTAs fit on device `dev` at once.
+int fp8_split_clusters(int dev, int splits);
 
 }  // namespace qlora

@@ -337,10 +337,31 @@ int launch_fp8_split(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w
   return w_mn ? launch<true>(tm_x, tm_w, p, st) : launch<false>(tm_x, tm_w, p, st);
 }
 
-cudaError_t set_fp8_split_attributes() {
-  const cudaError_t e = cudaFuncSetAttribute(k_fp8_split<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_fp8_split<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+namespace {
+int g_clusters[64][kFp8MaxSplits + 1];   // written by the device check, under its lock
 }
+
+cudaError_t set_fp8_split_attributes(int dev) {
+  cudaError_t e = cudaFuncSetAttribute(k_fp8_split<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_fp8_split<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  for (int s = 1; e == cudaSuccess && s <= kFp8MaxSplits; ++s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&g_clusters[dev][s], k_fp8_split<false>, &cfg);
+  }
+  return e;
+}
+
+int fp8_split_clusters(int dev, int splits) { return g_clusters[dev][splits]; }
 
 }  // namespace qlora

@@ -15,7 +15,7 @@ int check_current_device(int* sms, int* pairs = nullptr);
 
 // Shared-memory limits of the 8-bit product's kernels (fp8.cu); part of the
 // device check, which sets every kernel's attributes once a context.
-cudaError_t set_fp8_attributes();
+cudaError_t set_fp8_attributes(int dev);
 
 // Device address of the status word (ptx.cuh) on the current device, after a
 // successful device check.
