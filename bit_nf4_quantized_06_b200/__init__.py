@@ -19,6 +19,7 @@ Functions carry the C names:
 """
 
 import ctypes
+import operator
 import os
 
 __all__ = [
@@ -136,9 +137,16 @@ def _check(status, where):
         raise QloraError(status, where)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    # imported on first use, kept: an import statement costs as much as a launch's arguments
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream):
@@ -407,6 +415,7 @@ def qlora_adamw_paged(grad_dev, master_host, m_host, v_host, grad_host, step, pa
 # call allocates then belongs to that stream.
 FP8_E4M3, FP8_E5M2 = 0, 1
 _STATE_BLOCK = 256
+_dtype_of = operator.attrgetter("dtype")
 
 
 class Fp8Struct(ctypes.Structure):
@@ -463,6 +472,11 @@ def _raw_stream(dev):
 
 def _is(t, dtype, shape, dev):
     return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _matrix(rows, cols, dtype, device):
+    # the cheapest of torch's allocating calls for a shape of two
+    return _torch().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _want(ok, where, what):
@@ -524,10 +538,13 @@ class FP8Rows:
     @classmethod
     def empty(cls, rows, cols, fmt=FP8_E4M3, device="cuda"):
         torch = _torch()
-        codes = torch.empty((rows, -(-cols // 16) * 16), dtype=_fp8_dtype(fmt), device=device)
-        if codes.shape[1] != cols:
-            codes = codes[:, :cols]
-        return cls(codes, torch.empty((rows, -(-cols // 128)), dtype=torch.float32, device=device))
+        dtype, ld = _fp8_dtype(fmt), -(-cols // 16) * 16
+        codes = _matrix(rows, ld, dtype, device)
+        self = cls.__new__(cls)      # right by construction: no checks
+        self.codes = codes if ld == cols else codes[:, :cols]
+        self.scales = _matrix(rows, -(-cols // 128), torch.float32, device)
+        self.ld, self.fmt = ld, int(fmt)
+        return self
 
     def struct(self):
         rows, cols = self.codes.shape
@@ -599,15 +616,16 @@ def _fp8_product(call, where, q, x, fmt, cols_in, cols_out, out, ws):
           f"rows must be FP8Rows or contiguous bf16 [m, {cols_in}] on the weight's device")
     m = src.shape[0]
     if out is None:
-        out = torch.empty((m, cols_out), dtype=torch.bfloat16, device=src.device)
+        out = _matrix(m, cols_out, torch.bfloat16, src.device)
     else:
         _want(_is(out, torch.bfloat16, (m, cols_out), dev), where, f"the output must be contiguous bf16 [m, {cols_out}]")
-    if ws is None:
-        ws = torch.empty(lib.qlora_fp8_workspace_bytes(m, q.n_out, q.k_in), dtype=torch.uint8, device=src.device)
-    else:
+    if ws is not None:
         _want(ws.get_device() == dev and ws.is_contiguous(), where, "the workspace must be contiguous, on the weight's device")
+    elif rows is None:           # rows already in 8 bits need none
+        ws = torch.empty(lib.qlora_fp8_workspace_bytes(m, q.n_out, q.k_in), dtype=torch.uint8, device=src.device)
+    at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     args = (q.struct(), None if rows is not None else x.data_ptr(), rows) + (() if fmt is None else (int(fmt),))
-    _check(call(*args, m, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev)), where)
+    _check(call(*args, m, out.data_ptr(), at, size, _raw_stream(dev)), where)
     return out
 
 
@@ -774,7 +792,7 @@ def qlora_adamw_multi(group, grads, step, lr=1e-4, betas=(0.9, 0.999), eps=1e-8,
         with at:
             return qlora_adamw_multi(group, grads, step, lr, betas, eps, weight_decay)
     _want(list(map(T.numel, grads)) == group.sizes, "qlora_adamw_multi", "grads must match the masters in number and length")
-    _want(all(g.dtype is torch.float32 for g in grads) and all(map(T.is_contiguous, grads)) and
+    _want(set(map(_dtype_of, grads)) == {torch.float32} and all(map(T.is_contiguous, grads)) and
           set(map(T.get_device, grads)) == {dev}, "qlora_adamw_multi", "grads must be contiguous fp32 on the group's device")
     _want(list(map(T.data_ptr, group.masters)) == group._at[0] and
           list(map(T.data_ptr, group.params or ())) == group._at[1], "qlora_adamw_multi",

@@ -24,6 +24,10 @@ __device__ __forceinline__ constexpr float fp8_top() {
   return FMT == kE4M3 ? 448.0f : 57344.0f;
 }
 
+// What a value that is not finite asks for costs nothing where there is none:
+// a maximum of fabsf ignores NaN, and NaN * inv converts to the NaN code; only
+// an infinity, which shows as an infinite maximum, needs the next two.
+//
 // |v| where v is finite, else 0: what enters a block's maximum
 __device__ __forceinline__ float fp8_mag(float v) {
   const float a = fabsf(v);

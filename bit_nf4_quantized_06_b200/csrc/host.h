@@ -17,6 +17,9 @@ int check_current_device(int* sms, int* pairs = nullptr);
 // device check, which sets every kernel's attributes once a context.
 cudaError_t set_fp8_attributes(int dev);
 
+// The same for the RMS norm's (norm.cu).
+cudaError_t set_norm_attributes();
+
 // Device address of the status word (ptx.cuh) on the current device, after a
 // successful device check.
 unsigned int* device_status_word();

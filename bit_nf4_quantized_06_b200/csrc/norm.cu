@@ -33,7 +33,7 @@ struct NormFwd {
   float* rstd;                 // may be null
   int64_t rows, d, ld;         // ld: bytes from row to row of codes
   int64_t nblk;                // scales per row
-  float eps;
+  float eps, inv_d;
 };
 
 struct NormBwd {
@@ -45,6 +45,8 @@ struct NormBwd {
   __nv_bfloat16* dx;
   float* part;                 // [gridDim.x][d], null without dgamma
   int64_t rows, d;
+  float inv_d;
+  int stages;                  // bulk stages; 0: plain loads
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -60,17 +62,17 @@ __device__ __forceinline__ float warp_sum(float v) {
 // access (d % 8 == 0); else columns c0 + lane + 32 j, so that 2-byte accesses
 // of a warp fall into one line. Packed as bf16 pairs (2i, 2i + 1).
 template <bool VEC>
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int64_t c0, int lane, int64_t d) {
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int c0, int lane, int d) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (VEC) {
-    const int64_t c = c0 + 8 * lane;
+    const int c = c0 + 8 * lane;
     if (c < d) v = *reinterpret_cast<const uint4*>(row + c);
   } else {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t c = c0 + lane + 32 * j;
+      const int c = c0 + lane + 32 * j;
       w[j] = c < d ? p[c] : 0u;
     }
     v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
@@ -79,16 +81,16 @@ __device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int64_t c0, int
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* row, int64_t c0, int lane, int64_t d, uint4 v) {
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int c0, int lane, int d, uint4 v) {
   if (VEC) {
-    const int64_t c = c0 + 8 * lane;
+    const int c = c0 + 8 * lane;
     if (c < d) *reinterpret_cast<uint4*>(row + c) = v;
   } else {
     uint16_t* p = reinterpret_cast<uint16_t*>(row);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t c = c0 + lane + 32 * j;
+      const int c = c0 + lane + 32 * j;
       if (c < d) p[c] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
     }
   }
@@ -110,46 +112,56 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // Quantize and store a lane's 8 values of a chunk: the chunk's two blocks of
 // 128 columns are lanes 0-15 and 16-31 (VEC) or values 0-3 and 4-7.
 template <bool VEC, int FMT>
-__device__ __forceinline__ void store_fp8(uint8_t* row, float* scales, int64_t c0, int lane, int64_t d, int64_t nblk,
-                                          const float (&f)[8]) {
+__device__ __forceinline__ void store_fp8(uint8_t* row, float* scales, int c0, int lane, int d, float (&f)[8]) {
   constexpr float F = fp8_top<FMT>();
-  const int64_t b0 = c0 / kFp8Block;
+  constexpr int NB = VEC ? 1 : 2;              // blocks that a lane has values of
+  constexpr int REACH = VEC ? 8 : 16;          // lanes that share a block: 16 or 32
+  float a[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    a[b] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8 / NB; ++j) a[b] = fmaxf(a[b], fabsf(f[8 / NB * b + j]));
+#pragma unroll
+    for (int o = REACH; o > 0; o >>= 1) a[b] = fmaxf(a[b], __shfl_xor_sync(0xFFFFFFFFu, a[b], o));
+  }
+  if (__any_sync(0xFFFFFFFFu, a[0] > FLT_MAX || a[NB - 1] > FLT_MAX)) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      a[b] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8 / NB; ++j) {
+        float& v = f[8 / NB * b + j];
+        a[b] = fmaxf(a[b], fp8_mag(v));
+        v += v - v;                            // an infinity becomes NaN
+      }
+#pragma unroll
+      for (int o = REACH; o > 0; o >>= 1) a[b] = fmaxf(a[b], __shfl_xor_sync(0xFFFFFFFFu, a[b], o));
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) a[b] = fmaxf(a[b], kFp8Least);
   if (VEC) {
-    float a = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a = fmaxf(a, fp8_mag(f[j]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    a = fmaxf(a, kFp8Least);
-    const float inv = F / a;
-    const int64_t c = c0 + 8 * lane;
+    const float inv = F / a[0];
+    const int c = c0 + 8 * lane;
     if (c < d) {
       uint2 q;
-      q.x = fp8_pack4<FMT>(fp8_scaled(f[0], inv), fp8_scaled(f[1], inv), fp8_scaled(f[2], inv), fp8_scaled(f[3], inv));
-      q.y = fp8_pack4<FMT>(fp8_scaled(f[4], inv), fp8_scaled(f[5], inv), fp8_scaled(f[6], inv), fp8_scaled(f[7], inv));
+      q.x = fp8_pack4<FMT>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+      q.y = fp8_pack4<FMT>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
       *reinterpret_cast<uint2*>(row + c) = q;
-      if ((lane & 15) == 0) scales[b0 + (lane >> 4)] = a / F;
+      if ((lane & 15) == 0) scales[c >> 7] = a[0] / F;
     }
   } else {
-    float a[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j >> 2] = fmaxf(a[j >> 2], fp8_mag(f[j]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a[0] = fmaxf(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], o));
-      a[1] = fmaxf(a[1], __shfl_xor_sync(0xFFFFFFFFu, a[1], o));
-    }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      a[b] = fmaxf(a[b], kFp8Least);
+    for (int b = 0; b < NB; ++b) {
       const float inv = F / a[b];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t c = c0 + lane + 32 * (4 * b + j);
-        const float s = fp8_scaled(f[4 * b + j], inv);
+        const int c = c0 + lane + 32 * (4 * b + j);
+        const float s = f[4 * b + j] * inv;
         if (c < d) row[c] = static_cast<uint8_t>(fp8_pack2<FMT>(s, s));
       }
-      if (lane == 0 && b0 + b < nblk) scales[b0 + b] = a[b] / F;
+      if (lane == 0 && c0 + 128 * b < d) scales[(c0 >> 7) + b] = a[b] / F;
     }
   }
 }
@@ -164,6 +176,37 @@ __device__ __forceinline__ float group_sum(float v, float* red, int warps) {
   return warp_sum(lane < warps ? red[lane] : 0.0f);
 }
 
+constexpr int kBwdMaxStages = 8;
+constexpr size_t kBwdMaxSmem = 220 * 1024;
+
+// Untiled bulk copy global -> this CTA's shared memory (16-byte aligned, a
+// multiple of 16 bytes), counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Bounded wait; on timeout sets the status bit and gives up.
+__device__ __forceinline__ bool bulk_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > QLORA_WAIT_LIMIT_NS) {
+      atomicOr(&g_dev_status, QLORA_DEV_TIMEOUT_PRODUCER);
+      return false;
+    }
+  return true;
+}
+
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
 enum NormOut : int { kOutBf16 = 0, kOutE4M3 = 1, kOutE5M2 = 2 };
 
 // NV chunks a warp, kept in registers; NV == 0: any width, h is read again
@@ -175,25 +218,35 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool live = row < p.rows;
-  const int64_t d = live ? p.d : 0;     // an idle group reads and writes nothing
+  const int d = live ? static_cast<int>(p.d) : 0;     // an idle group reads and writes nothing
+  const int width = static_cast<int>(p.d);
   const __nv_bfloat16* x = p.x + row * p.d;
   const __nv_bfloat16* res = p.res + row * p.d;
   constexpr int KEEP = NV > 0 ? NV : 1;
-  const int64_t step = static_cast<int64_t>(warps) * kChunk;
-  const int64_t nstep = NV > 0 ? NV : (p.d + step - 1) / step;
+  const int step = warps * kChunk;
+  const int nstep = NV > 0 ? NV : (width + step - 1) / step;
   uint4 keep[KEEP];
   grid_dependency_wait();
   grid_dependency_trigger();
 
+  // both in packed pairs: this kernel is as much bound by issue as by HBM
   auto add = [&](uint4 a, uint4 b) {
-    float fa[8], fb[8];
-    unpack8(a, fa);
-    unpack8(b, fb);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) fa[j] += fb[j];
-    return pack8(fa);
+    auto pair = [](uint32_t u, uint32_t v) {
+      uint32_t lo, hi;
+      f2_split(f2_add(f2(bf_lo(u), bf_hi(u)), f2(bf_lo(v), bf_hi(v))), lo, hi);
+      return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+    };
+    return make_uint4(pair(a.x, b.x), pair(a.y, b.y), pair(a.z, b.z), pair(a.w, b.w));
   };
-  float sum = 0.0f;
+  uint64_t sum2 = 0;
+  auto square = [&](uint4 t) {
+    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t v = f2(bf_lo(w[i]), bf_hi(w[i]));
+      sum2 = f2_fma(v, v, sum2);
+    }
+  };
   if constexpr (NV > 0) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) keep[v] = load8<VEC>(x, v * step + warp * kChunk, lane, d);
@@ -209,37 +262,32 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
     }
     if (NORM) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float f[8];
-        unpack8(keep[v], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
-      }
+      for (int v = 0; v < NV; ++v) square(keep[v]);
     }
   } else if (NORM) {
-    for (int64_t v = 0; v < nstep; ++v) {
-      const int64_t c0 = v * step + warp * kChunk;
+    for (int v = 0; v < nstep; ++v) {
+      const int c0 = v * step + warp * kChunk;
       uint4 t = load8<VEC>(x, c0, lane, d);
       if (p.res != nullptr) {
         t = add(t, load8<VEC>(res, c0, lane, d));
         store8<VEC>(p.h + row * p.d, c0, lane, d, t);
       }
-      float f[8];
-      unpack8(t, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+      square(t);
     }
   }
   float rstd = 1.0f;
   if (NORM) {
-    sum = group_sum(sum, s_red + 32 * threadIdx.y, warps);
-    rstd = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+    uint32_t lo, hi;
+    f2_split(sum2, lo, hi);
+    const float sum = group_sum(__uint_as_float(lo) + __uint_as_float(hi), s_red + 32 * threadIdx.y, warps);
+    rstd = rsqrtf(fmaf(sum, p.inv_d, p.eps));
     if (live && threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
   }
+  const uint64_t rstd2 = f2(rstd, rstd);
 #pragma unroll
-  for (int64_t v = 0; v < nstep; ++v) {
-    const int64_t c0 = v * step + warp * kChunk;
-    if (c0 >= p.d) break;
+  for (int v = 0; v < nstep; ++v) {
+    const int c0 = v * step + warp * kChunk;
+    if (c0 >= width) break;
     uint4 t;
     if constexpr (NV > 0) {
       t = keep[v];
@@ -248,92 +296,158 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
       t = load8<VEC>(NORM && p.res != nullptr ? p.h + row * p.d : x, c0, lane, d);
     }
     float f[8];
-    unpack8(t, f);
     if (NORM) {
-      float g[8];
-      unpack8(load8<VEC>(p.gamma, c0, lane, p.d), g);
+      const uint4 g = load8<VEC>(p.gamma, c0, lane, width);
+      const uint32_t tw[4] = {t.x, t.y, t.z, t.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * g[j];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo, hi;
+        f2_split(f2_mul(f2_mul(f2(bf_lo(tw[i]), bf_hi(tw[i])), rstd2), f2(bf_lo(gw[i]), bf_hi(gw[i]))), lo, hi);
+        f[2 * i] = __uint_as_float(lo);
+        f[2 * i + 1] = __uint_as_float(hi);
+      }
+    } else {
+      unpack8(t, f);
     }
     if (OUT == kOutBf16)
       store8<VEC>(p.y + row * p.d, c0, lane, d, pack8(f));
     else
-      store_fp8<VEC, OUT == kOutE5M2 ? kE5M2 : kE4M3>(p.codes + row * p.ld, p.scales + row * p.nblk, c0, lane, d,
-                                                      live ? p.nblk : 0, f);
+      store_fp8<VEC, OUT == kOutE5M2 ? kE5M2 : kE4M3>(p.codes + row * p.ld, p.scales + row * p.nblk, c0, lane, d, f);
   }
 }
 
-// Gradients. A CTA of up to 512 threads holds groups of T threads; group y
-// takes rows y, y + groups, ... A thread's columns are the same in every row,
-// so its share of dgamma stays in registers until the CTA's groups are added
-// up through shared memory, in a fixed order, into one partial row a CTA;
-// k_dgamma adds the CTAs' rows. NV == 0: any width, the partial row is kept in
-// global memory (one group a CTA, each thread its own columns).
-template <int NV, bool VEC>
+// Gradients. A CTA of up to 512 threads holds groups of T threads, a row each.
+// A thread's columns are the same in every row, so its share of dgamma stays
+// in registers until the CTA's groups are added up through shared memory, in a
+// fixed order, into one partial row a CTA; k_dgamma adds the CTAs' rows.
+//
+// BULK (rows of whole 16-byte pieces that fit): the rows come through a ring
+// of p.stages stages in shared memory, filled by bulk copies, and are read
+// from there twice, for the row sum and for the output. The barrier of a
+// round's row sum shows that the round before is done with its stage; one
+// thread then refills it. Otherwise (odd widths, and NV == 0: wide rows, whose
+// partial row is kept in global memory) plain loads.
+template <int NV, bool VEC, bool BULK>
 __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
-  extern __shared__ float s_part[];      // NV > 0 and more than one group: d floats
+  extern __shared__ __align__(16) uint8_t s_dyn[];   // BULK: the stages; then d floats for the groups' dgamma
   __shared__ float s_red[2][16 * 16];
+  __shared__ __align__(8) uint64_t s_bar[kBwdMaxStages];
+  static_assert(!BULK || (VEC && NV > 0), "bulk copies are for whole rows in registers");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   constexpr int KEEP = NV > 0 ? NV : 1;
-  const int64_t step = static_cast<int64_t>(warps) * kChunk;
-  const int64_t nstep = NV > 0 ? NV : (p.d + step - 1) / step;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * blockDim.y;
-  const float inv_d = 1.0f / static_cast<float>(p.d);
+  const int width = static_cast<int>(p.d);
+  const int step = warps * kChunk;
+  const int nstep = NV > 0 ? NV : (width + step - 1) / step;
+  const int groups = static_cast<int>(blockDim.y);
+  const bool one = threadIdx.x == 0 && threadIdx.y == 0;
+  const uint32_t row_bytes = static_cast<uint32_t>(width) * 2;
+  const int parts = p.dres != nullptr ? 3 : 2;
+  const uint32_t group_bytes = 3 * row_bytes, stage_bytes = groups * group_bytes;
+  const uint32_t dyn = smem_u32(s_dyn);
   float acc[KEEP][8];
 #pragma unroll
   for (int v = 0; v < KEEP; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[v][j] = 0.0f;
+  if (BULK && one) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&s_bar[s]), 1);
+    fence_mbar_init();
+  }
+  if (BULK) __syncthreads();
   grid_dependency_wait();
   grid_dependency_trigger();
   float* prow = p.part == nullptr ? nullptr : p.part + blockIdx.x * p.d;
 
   // every group of the CTA runs the same number of rounds: the barrier of the
   // row sum is the whole CTA's
-  const int64_t rounds = (p.rows + groups - 1) / groups;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t rounds = (p.rows + stride - 1) / stride;
+  auto first_row = [&](int64_t i) { return (i * gridDim.x + blockIdx.x) * groups; };
+  auto fill = [&](int64_t i, int stage) {          // one thread: round i's rows
+    const int n = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(groups), p.rows - first_row(i))));
+    const uint32_t bar = smem_u32(&s_bar[stage]);
+    mbar_arrive_expect_tx(bar, n * parts * row_bytes);
+    for (int g = 0; g < n; ++g) {
+      const uint32_t dst = dyn + stage * stage_bytes + g * group_bytes;
+      const int64_t at = (first_row(i) + g) * p.d;
+      bulk_load(dst, p.dy + at, row_bytes, bar);
+      bulk_load(dst + row_bytes, p.h + at, row_bytes, bar);
+      if (parts == 3) bulk_load(dst + 2 * row_bytes, p.dres + at, row_bytes, bar);
+    }
+  };
+  if (BULK && one)
+    for (int i = 0; i < p.stages && i < rounds; ++i) fill(i, i);
+  uint4 kg[KEEP];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) kg[v] = load8<VEC>(p.gamma, v * step + warp * kChunk, lane, width);
+  }
+
+  int stage = 0;
+  uint32_t phase = 0;
+  float next_rstd = first_row(0) + threadIdx.y < p.rows ? p.rstd[first_row(0) + threadIdx.y] : 0.0f;
   for (int64_t i = 0; i < rounds; ++i) {
-    const int64_t row = (i * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t row = first_row(i) + threadIdx.y;
     const bool live = row < p.rows;
-    const int64_t d = live ? p.d : 0;
+    const int d = live ? width : 0;
     const __nv_bfloat16* dy = p.dy + row * p.d;
     const __nv_bfloat16* h = p.h + row * p.d;
-    const float rstd = live ? p.rstd[row] : 0.0f;
+    const float rstd = next_rstd;       // fetched a round ahead
+    if (row + stride < p.rows) next_rstd = p.rstd[row + stride];
     uint4 kdy[KEEP], kh[KEEP], kres[KEEP];
     float dot = 0.0f;
-    if constexpr (NV > 0) {
+    const uint32_t src = dyn + stage * stage_bytes + threadIdx.y * group_bytes;
+    if constexpr (BULK) {
+      if (!bulk_wait(smem_u32(&s_bar[stage]), phase)) return;
+    } else if constexpr (NV > 0) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int64_t c0 = v * step + warp * kChunk;
+        const int c0 = v * step + warp * kChunk;
         kdy[v] = load8<VEC>(dy, c0, lane, d);
         kh[v] = load8<VEC>(h, c0, lane, d);
-        if (p.dres != nullptr) kres[v] = load8<VEC>(p.dres + row * p.d, c0, lane, d);
+        if (parts == 3) kres[v] = load8<VEC>(p.dres + row * p.d, c0, lane, d);
       }
     }
+    // part 0 dy, 1 h, 2 dres: this lane's 8 values of a chunk
+    auto fetch = [&](int part, int v, int c0) -> uint4 {
+      if constexpr (BULK) {
+        const int c = c0 + 8 * lane;
+        return c < d ? lds_u4(src + part * row_bytes + 2 * c) : make_uint4(0, 0, 0, 0);
+      } else if constexpr (NV > 0) {
+        return part == 0 ? kdy[v] : part == 1 ? kh[v] : kres[v];
+      } else {
+        return load8<VEC>(part == 0 ? dy : part == 1 ? h : p.dres + row * p.d, c0, lane, d);
+      }
+    };
+    auto values = [&](int v, int c0, float (&a)[8], float (&b)[8], float (&g)[8]) {
+      unpack8(fetch(0, v, c0), a);
+      unpack8(fetch(1, v, c0), b);
+      unpack8(NV > 0 ? kg[NV > 0 ? v : 0] : load8<VEC>(p.gamma, c0, lane, width), g);
+    };
 #pragma unroll
-    for (int64_t v = 0; v < nstep; ++v) {
-      const int64_t c0 = v * step + warp * kChunk;
+    for (int v = 0; v < nstep; ++v) {
       float a[8], b[8], g[8];
-      unpack8(NV > 0 ? kdy[NV > 0 ? v : 0] : load8<VEC>(dy, c0, lane, d), a);
-      unpack8(NV > 0 ? kh[NV > 0 ? v : 0] : load8<VEC>(h, c0, lane, d), b);
-      unpack8(load8<VEC>(p.gamma, c0, lane, p.d), g);
+      values(v, v * step + warp * kChunk, a, b, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) dot = fmaf(a[j] * g[j], b[j], dot);
     }
     // two buffers in turn: a warp that is a round ahead does not overwrite sums still being read
     dot = group_sum(dot, s_red[i & 1] + 16 * threadIdx.y, warps);
-    const float c = dot * inv_d * rstd * rstd;
+    if (BULK) {
+      if (warps == 1) __syncthreads();     // with one warp a group the sum has no barrier
+      if (one && i > 0 && i - 1 + p.stages < rounds) fill(i - 1 + p.stages, stage == 0 ? p.stages - 1 : stage - 1);
+    }
+    const float c = dot * p.inv_d * rstd * rstd;
 #pragma unroll
-    for (int64_t v = 0; v < nstep; ++v) {
-      const int64_t c0 = v * step + warp * kChunk;
+    for (int v = 0; v < nstep; ++v) {
+      const int c0 = v * step + warp * kChunk;
       float a[8], b[8], g[8], o[8];
-      unpack8(NV > 0 ? kdy[NV > 0 ? v : 0] : load8<VEC>(dy, c0, lane, d), a);
-      unpack8(NV > 0 ? kh[NV > 0 ? v : 0] : load8<VEC>(h, c0, lane, d), b);
-      unpack8(load8<VEC>(p.gamma, c0, lane, p.d), g);
+      values(v, c0, a, b, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (a[j] * g[j] - b[j] * c) * rstd;
-      if (p.dres != nullptr) {
+      if (parts == 3) {
         float r[8];
-        unpack8(NV > 0 ? kres[NV > 0 ? v : 0] : load8<VEC>(p.dres + row * p.d, c0, lane, d), r);
+        unpack8(fetch(2, v, c0), r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] += r[j];
       }
@@ -346,24 +460,30 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
       } else if (prow != nullptr && live) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int64_t col = c0 + (VEC ? 8 * lane + j : lane + 32 * j);
+          const int col = c0 + (VEC ? 8 * lane + j : lane + 32 * j);
           if (col < d) prow[col] = fmaf(a[j], b[j] * rstd, i == 0 ? 0.0f : prow[col]);
         }
       }
     }
+    if (BULK && ++stage == p.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
   }
   if constexpr (NV > 0) {
     if (prow == nullptr) return;
-    for (int y = 0; y < static_cast<int>(blockDim.y); ++y) {
+    float* s_part = reinterpret_cast<float*>(s_dyn);
+    __syncthreads();                    // the stages are read: their memory takes the groups' sums
+    for (int y = 0; y < groups; ++y) {
       if (static_cast<int>(threadIdx.y) == y) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int64_t col = v * step + warp * kChunk + (VEC ? 8 * lane + j : lane + 32 * j);
-            if (col < p.d) {
+            const int col = v * step + warp * kChunk + (VEC ? 8 * lane + j : lane + 32 * j);
+            if (col < width) {
               const float t = y == 0 ? acc[v][j] : s_part[col] + acc[v][j];
-              if (y + 1 < static_cast<int>(blockDim.y))
+              if (y + 1 < groups)
                 s_part[col] = t;
               else
                 prow[col] = t;
@@ -421,45 +541,70 @@ int launch_rows_vec(const NormFwd& p, cudaStream_t st) {
   return p.d % 8 == 0 ? launch_rows<true, OUT, NORM>(p, st) : launch_rows<false, OUT, NORM>(p, st);
 }
 
-// The backward's CTA: T threads a row, as many groups as 512 threads hold.
+// The backward's CTA: T threads a row, as many groups as 512 threads hold, and
+// as many bulk stages (three rows a group each) as fit, at least two.
 struct BwdPlan {
   int nv, t, r;
   int grid;
+  int stages;
 };
 
 BwdPlan plan_bwd(int64_t rows, int64_t d, int sms) {
   BwdPlan b;
-  b.nv = d <= kChunk ? 1 : d <= 2 * 16 * kChunk ? 2 : d <= 4 * 16 * kChunk ? 4 : 0;
+  // widths of 8192 to 16384 only through bulk stages: without them four chunks a warp do not fit the registers
+  b.nv = d <= kChunk ? 1 : d <= 2 * 16 * kChunk ? 2 : d <= 4 * 16 * kChunk && d % 8 == 0 ? 4 : 0;
   b.t = b.nv == 0 ? 512 : static_cast<int>(cdiv(d, int64_t(kChunk) * b.nv)) * 32;
   b.r = b.nv == 0 ? 1 : std::max(1, 512 / b.t);
   b.grid = static_cast<int>(std::min<int64_t>(sms, cdiv(rows, b.r)));
+  b.stages = b.nv > 0 && d % 8 == 0
+                 ? static_cast<int>(std::min<int64_t>(kBwdMaxStages, kBwdMaxSmem / (static_cast<int64_t>(b.r) * 6 * d)))
+                 : 0;
+  if (b.stages < 2) b.stages = 0;
   return b;
 }
 
-template <int NV, bool VEC>
+template <int NV, bool VEC, bool BULK>
 int launch_bwd_nv(const BwdPlan& b, const NormBwd& p, cudaStream_t st) {
-  const size_t smem = NV > 0 && b.r > 1 ? static_cast<size_t>(p.d) * sizeof(float) : 0;
-  return host::launch_pdl(k_rmsnorm_bwd<NV, VEC>, dim3(b.grid), dim3(b.t, b.r), smem, st, 1, p);
+  const size_t sums = NV > 0 && b.r > 1 ? static_cast<size_t>(p.d) * sizeof(float) : 0;
+  const size_t smem = std::max(static_cast<size_t>(b.stages) * b.r * 6 * p.d, sums);
+  return host::launch_pdl(k_rmsnorm_bwd<NV, VEC, BULK>, dim3(b.grid), dim3(b.t, b.r), smem, st, 1, p);
 }
 
-template <bool VEC>
 int launch_bwd(const BwdPlan& b, const NormBwd& p, cudaStream_t st) {
+  if (b.stages > 0) {
+    switch (b.nv) {
+      case 1: return launch_bwd_nv<1, true, true>(b, p, st);
+      case 2: return launch_bwd_nv<2, true, true>(b, p, st);
+      default: return launch_bwd_nv<4, true, true>(b, p, st);
+    }
+  }
+  if (p.d % 8 == 0) return launch_bwd_nv<0, true, false>(b, p, st);
   switch (b.nv) {
-    case 1: return launch_bwd_nv<1, VEC>(b, p, st);
-    case 2: return launch_bwd_nv<2, VEC>(b, p, st);
-    case 4: return launch_bwd_nv<4, VEC>(b, p, st);
-    default: return launch_bwd_nv<0, VEC>(b, p, st);
+    case 1: return launch_bwd_nv<1, false, false>(b, p, st);
+    case 2: return launch_bwd_nv<2, false, false>(b, p, st);
+    default: return launch_bwd_nv<0, false, false>(b, p, st);
   }
 }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxCols = int64_t(1) << 30;    // columns are 32-bit numbers in the kernels
 
 }  // namespace
+
+cudaError_t set_norm_attributes() {
+  const int n = static_cast<int>(kBwdMaxSmem);
+  cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd<1, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_rmsnorm_bwd<2, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_rmsnorm_bwd<4, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  return e;
+}
 
 qlora_status_t check_fp8_rows(const qlora_fp8_rows_t* r) {
   if (r == nullptr || r->reserved != 0) return QLORA_ERR_INVALID_ARG;
   if (r->format != QLORA_FP8_E4M3 && r->format != QLORA_FP8_E5M2) return QLORA_ERR_INVALID_ARG;
-  if (r->rows < 0 || r->rows > kMaxRows || r->cols < 1 || r->cols > kMaxRows) return QLORA_ERR_SHAPE;
+  if (r->rows < 0 || r->rows > kMaxRows || r->cols < 1 || r->cols > kMaxCols) return QLORA_ERR_SHAPE;
   if (r->ld < r->cols || r->ld % 16 != 0) return QLORA_ERR_SHAPE;
   if (r->rows == 0) return QLORA_OK;
   if (r->codes == nullptr || r->scales == nullptr) return QLORA_ERR_INVALID_ARG;
@@ -500,7 +645,7 @@ qlora_status_t qlora_quantize_fp8_rows(const void* x_bf16, const qlora_fp8_rows_
 qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
                                  int64_t d, float eps, void* h_out_bf16, void* y_bf16, const qlora_fp8_rows_t* y8,
                                  float* rstd_out, void* stream) {
-  if (rows < 0 || rows > kMaxRows || d < 1 || d > kMaxRows) return QLORA_ERR_SHAPE;
+  if (rows < 0 || rows > kMaxRows || d < 1 || d > kMaxCols) return QLORA_ERR_SHAPE;
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return QLORA_ERR_INVALID_ARG;
   if (y8 != nullptr) {
     const qlora_status_t s = check_fp8_rows(y8);
@@ -527,6 +672,7 @@ qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, 
   p.rows = rows;
   p.d = d;
   p.eps = eps;
+  p.inv_d = static_cast<float>(1.0 / static_cast<double>(d));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (y8 == nullptr) return static_cast<qlora_status_t>(launch_rows_vec<kOutBf16, true>(p, st));
   p.codes = y8->codes;
@@ -538,7 +684,7 @@ qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, 
 }
 
 size_t qlora_rmsnorm_workspace_bytes(int64_t rows, int64_t d) {
-  if (rows < 1 || rows > kMaxRows || d < 1 || d > kMaxRows) return 0;
+  if (rows < 1 || rows > kMaxRows || d < 1 || d > kMaxCols) return 0;
   int sms = 0;
   if (check_current_device(&sms) != QLORA_OK) sms = 148;
   return static_cast<size_t>(plan_bwd(rows, d, sms).grid) * static_cast<size_t>(d) * sizeof(float);
@@ -547,7 +693,7 @@ size_t qlora_rmsnorm_workspace_bytes(int64_t rows, int64_t d) {
 qlora_status_t qlora_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16, const float* rstd,
                                  const void* dres_bf16, int64_t rows, int64_t d, void* dx_bf16, float* dgamma,
                                  void* ws, size_t ws_bytes, void* stream) {
-  if (rows < 0 || rows > kMaxRows || d < 1 || d > kMaxRows) return QLORA_ERR_SHAPE;
+  if (rows < 0 || rows > kMaxRows || d < 1 || d > kMaxCols) return QLORA_ERR_SHAPE;
   if (!aligned(dgamma, 16)) return QLORA_ERR_ALIGNMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   qlora_status_t s;
@@ -578,7 +724,9 @@ qlora_status_t qlora_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const 
   p.part = dgamma == nullptr ? nullptr : static_cast<float*>(ws);
   p.rows = rows;
   p.d = d;
-  s = static_cast<qlora_status_t>(d % 8 == 0 ? launch_bwd<true>(b, p, st) : launch_bwd<false>(b, p, st));
+  p.inv_d = static_cast<float>(1.0 / static_cast<double>(d));
+  p.stages = b.stages;
+  s = static_cast<qlora_status_t>(launch_bwd(b, p, st));
   if (s != QLORA_OK || dgamma == nullptr) return s;
   return static_cast<qlora_status_t>(host::launch_pdl(k_dgamma, rgrid, rblock, 0, st, 1,
                                                       static_cast<const float*>(ws), b.grid, d, dgamma));

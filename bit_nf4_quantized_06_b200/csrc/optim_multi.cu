@@ -58,24 +58,59 @@ struct Multi {
 constexpr int kCapSmall = 24, kCapLarge = 470;
 static_assert(sizeof(Multi<kCapLarge>) <= 32764, "kernel parameter block");
 
-__device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, bool vec, const AdamwHyper& hp) {
-  // values i0 + 8 lane + j of the block that starts at i0
+__device__ __forceinline__ float sqrt_approx(float v) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) {
+  uint32_t a, b;
+  f2_split(v, a, b);
+  return __uint_as_float(a);
+}
+__device__ __forceinline__ float hi_of(uint64_t v) {
+  uint32_t a, b;
+  f2_split(v, a, b);
+  return __uint_as_float(b);
+}
+
+// Constants of the 8-bit step, in pairs.
+struct Hyper2 {
+  uint64_t beta1, gain1, beta2, gain2, decay, neg_step, inv_sqrt_bc2, eps;
+};
+__device__ __forceinline__ Hyper2 hyper2(const AdamwHyper& a) {
+  auto two = [](float v) { return f2(v, v); };
+  return Hyper2{two(a.beta1), two(1.0f - a.beta1), two(a.beta2), two(1.0f - a.beta2), two(a.decay),
+                two(-a.step_size), two(a.inv_sqrt_bc2), two(a.eps)};
+}
+
+// The block of 256 values at i0: eight values a lane, in packed pairs, with
+// the hardware's square root and reciprocal (off by a step or two of fp32, far
+// below a code's own rounding and below p's in the update): with the exact
+// ones this kernel was bound by issue (83 instructions a value, 654 us for
+// 160 million values; see the table of cases for the time now).
+__device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, bool vec, const Hyper2& hp) {
   const int64_t at = i0 + 8 * lane;
   const int64_t blk = i0 / kStateBlock;
   const int valid = static_cast<int>(min(static_cast<int64_t>(8), max(static_cast<int64_t>(0), t.n - at)));
   const float ms = t.m_scales[blk], vs = t.v_scales[blk];
   uint8_t* mc = static_cast<uint8_t*>(t.m) + at;
   uint8_t* vc = static_cast<uint8_t*>(t.v) + at;
-  float p[8], g[8], m[8], r[8];
   const bool wide = vec && valid == 8;
-  uint2 mq = make_uint2(0, 0), vq = make_uint2(0, 0);
+  float p[8], g[8];
+  uint2 mq, vq;
   if (wide) {
-    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(t.master + at);
-    *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(t.master + at + 4);
     *reinterpret_cast<float4*>(g) = __ldcs(reinterpret_cast<const float4*>(t.grad + at));
     *reinterpret_cast<float4*>(g + 4) = __ldcs(reinterpret_cast<const float4*>(t.grad + at + 4));
     mq = *reinterpret_cast<const uint2*>(mc);
     vq = *reinterpret_cast<const uint2*>(vc);
+    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(t.master + at);
+    *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(t.master + at + 4);
   } else {
     uint32_t mb[8], vb[8];
 #pragma unroll
@@ -89,28 +124,49 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
     mq = make_uint2(mb[0] | mb[1] << 8 | mb[2] << 16 | mb[3] << 24, mb[4] | mb[5] << 8 | mb[6] << 16 | mb[7] << 24);
     vq = make_uint2(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24, vb[4] | vb[5] << 8 | vb[6] << 16 | vb[7] << 24);
   }
+  const uint64_t ms2 = f2(ms, ms), vs2 = f2(vs, vs);
+  float m[8], r[8];
   float am = 0.0f, av = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const uint32_t sh = 8 * (j & 3);
     const float2 mm = fp8_unpack2<kE4M3>((j < 4 ? mq.x : mq.y) >> sh);
     const float2 rr = fp8_unpack2<kE4M3>((j < 4 ? vq.x : vq.y) >> sh);
-    m[j] = mm.x * ms;
-    m[j + 1] = mm.y * ms;
-    r[j] = rr.x * vs;
-    r[j + 1] = rr.y * vs;
-#pragma unroll
-    for (int e = j; e < j + 2; ++e) {
-      float v = r[e] * r[e];
-      p[e] = adamw_update(p[e], g[e], m[e], v, r[e], hp);
-      am = fmaxf(am, fp8_mag(m[e]));
-      av = fmaxf(av, fp8_mag(r[e]));
-    }
+    const uint64_t g2 = f2(g[j], g[j + 1]);
+    const uint64_t m2 = f2_fma(hp.beta1, f2_mul(f2(mm.x, mm.y), ms2), f2_mul(hp.gain1, g2));
+    const uint64_t r2 = f2_mul(f2(rr.x, rr.y), vs2);
+    const uint64_t v2 = f2_fma(hp.beta2, f2_mul(r2, r2), f2_mul(f2_mul(hp.gain2, g2), g2));
+    r[j] = sqrt_approx(lo_of(v2));
+    r[j + 1] = sqrt_approx(hi_of(v2));
+    const uint64_t d2 = f2_fma(f2(r[j], r[j + 1]), hp.inv_sqrt_bc2, hp.eps);
+    const uint64_t q2 = f2_mul(m2, f2(rcp_approx(lo_of(d2)), rcp_approx(hi_of(d2))));
+    const uint64_t p2 = f2_fma(hp.neg_step, q2, f2_mul(f2(p[j], p[j + 1]), hp.decay));
+    p[j] = lo_of(p2);
+    p[j + 1] = hi_of(p2);
+    m[j] = lo_of(m2);
+    m[j + 1] = hi_of(m2);
+    am = fmaxf(am, fmaxf(fabsf(m[j]), fabsf(m[j + 1])));
+    av = fmaxf(av, fmaxf(r[j], r[j + 1]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
     av = fmaxf(av, __shfl_xor_sync(0xFFFFFFFFu, av, o));
+  }
+  if (fmaxf(am, av) > FLT_MAX) {               // the same for the whole warp: infinities become NaN
+    am = av = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      am = fmaxf(am, fp8_mag(m[j]));
+      av = fmaxf(av, fp8_mag(r[j]));
+      m[j] += m[j] - m[j];
+      r[j] += r[j] - r[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+      av = fmaxf(av, __shfl_xor_sync(0xFFFFFFFFu, av, o));
+    }
   }
   constexpr float F = 448.0f;
   am = fmaxf(am, kFp8Least);
@@ -118,15 +174,15 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
   const float im = F / am, iv = F / av;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    m[j] = fp8_scaled(m[j], im);
+    m[j] *= im;
     const float c = r[j] * iv;
-    r[j] = (r[j] > 0.0f ? fmaxf(c, kLeastRoot) : c) + (r[j] - r[j]);   // NaN where the root is not finite
+    r[j] = r[j] > 0.0f ? fmaxf(c, kLeastRoot) : c;
   }
   mq = make_uint2(fp8_pack4<kE4M3>(m[0], m[1], m[2], m[3]), fp8_pack4<kE4M3>(m[4], m[5], m[6], m[7]));
   vq = make_uint2(fp8_pack4<kE4M3>(r[0], r[1], r[2], r[3]), fp8_pack4<kE4M3>(r[4], r[5], r[6], r[7]));
-  if (lane == 0) {
-    t.m_scales[blk] = am / F;
-    t.v_scales[blk] = av / F;
+  if (lane < 2) {
+    float* scale = lane == 0 ? t.m_scales : t.v_scales;
+    scale[blk] = (lane == 0 ? am : av) / F;
   }
   if (wide) {
     *reinterpret_cast<float4*>(t.master + at) = *reinterpret_cast<const float4*>(p);
@@ -184,6 +240,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw_multi(const __grid_constant_
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Hyper2 hp2 = hyper2(a.hp);
   for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     // the last tensor whose first chunk is not past c
     int lo = 0, hi = a.count - 1;
@@ -201,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw_multi(const __grid_constant_
 #pragma unroll
       for (int s = 0; s < kChunkValues / (kThreads * 8); ++s) {
         const int64_t b0 = i0 + (s * (kThreads / 32) + warp) * kStateBlock;
-        if (b0 < t.n) step8(t, b0, lane, vec, a.hp);
+        if (b0 < t.n) step8(t, b0, lane, vec, hp2);
       }
     } else {
 #pragma unroll
