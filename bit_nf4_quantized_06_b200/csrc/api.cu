@@ -230,6 +230,7 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
                                static_cast<int>(merge_tc_smem_bytes()));
     if (e == cudaSuccess) e = set_fp8_attributes(dev);
     if (e == cudaSuccess) e = set_norm_attributes();
+    if (e == cudaSuccess) e = set_adamw_attributes();
     if (e == cudaSuccess) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&st.status), g_dev_status);
     if (e != cudaSuccess) return QLORA_ERR_CUDA;
     st.attrs = true;

@@ -20,6 +20,9 @@ cudaError_t set_fp8_attributes(int dev);
 // The same for the RMS norm's (norm.cu).
 cudaError_t set_norm_attributes();
 
+// And the many-tensor AdamW's (optim_multi.cu).
+cudaError_t set_adamw_attributes();
+
 // Device address of the status word (ptx.cuh) on the current device, after a
 // successful device check.
 unsigned int* device_status_word();

@@ -12,6 +12,7 @@
 
 #include <cuda_bf16.h>
 
+#include "bulk.cuh"
 #include "fp8_dev.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -178,34 +179,6 @@ __device__ __forceinline__ float group_sum(float v, float* red, int warps) {
 
 constexpr int kBwdMaxStages = 8;
 constexpr size_t kBwdMaxSmem = 220 * 1024;
-
-// Untiled bulk copy global -> this CTA's shared memory (16-byte aligned, a
-// multiple of 16 bytes), counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-// Bounded wait; on timeout sets the status bit and gives up.
-__device__ __forceinline__ bool bulk_wait(uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer_ns() - t0 > QLORA_WAIT_LIMIT_NS) {
-      atomicOr(&g_dev_status, QLORA_DEV_TIMEOUT_PRODUCER);
-      return false;
-    }
-  return true;
-}
-
-__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 
 enum NormOut : int { kOutBf16 = 0, kOutE4M3 = 1, kOutE5M2 = 2 };
 

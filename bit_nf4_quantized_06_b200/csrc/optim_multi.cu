@@ -13,7 +13,13 @@
 // divide by eps alone. The step uses the new m and v in fp32, so rounding
 // them to 8 bits acts on later steps only.
 //
-// Bound by HBM: 30 bytes a value (32 bits, with the bf16 copy) or 18.1 (8 bits).
+// Bound by HBM: 30 bytes a value (32 bits, with the bf16 copy) or 18.1 (8
+// bits). A CTA takes chunks of eight blocks, a block a warp, through a ring of
+// stages in shared memory: one stage holds a chunk's master values, gradients
+// and states, filled by four bulk copies that are requested several chunks
+// ahead. (8 bits, 160 million values: loads to registers kept 61 KB in flight
+// on an SM, 573 us; a ring a warp, of 256-byte copies, was bound by the copies'
+// number, 816 us.)
 #include <algorithm>
 #include <cmath>
 #include <vector>
@@ -22,6 +28,7 @@
 
 #include "../../include/qlora.h"
 #include "adamw_math.cuh"
+#include "bulk.cuh"
 #include "fp8_dev.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -31,7 +38,7 @@ namespace {
 
 constexpr int kStateBlock = QLORA_ADAMW_STATE_BLOCK;
 constexpr int kThreads = 256;
-constexpr int kChunkValues = 4096;   // values of one chunk: a CTA's unit of work
+constexpr int kChunk = kThreads / 32 * kStateBlock;   // values of a chunk
 constexpr float kLeastRoot = 1.0f / 512.0f;   // the smallest e4m3 code above zero
 
 struct MultiTensor {
@@ -50,7 +57,7 @@ struct MultiTensor {
 template <int CAP>
 struct Multi {
   MultiTensor t[CAP];
-  int32_t first[CAP];       // the tensor's first chunk; bit 31: wide loads allowed
+  int32_t first[CAP];       // the tensor's first chunk in the list of all; bit 31: wide accesses allowed
   int32_t count;
   int32_t chunks;
   AdamwHyper hp;
@@ -89,41 +96,53 @@ __device__ __forceinline__ Hyper2 hyper2(const AdamwHyper& a) {
                 two(-a.step_size), two(a.inv_sqrt_bc2), two(a.eps)};
 }
 
-// The block of 256 values at i0: eight values a lane, in packed pairs, with
-// the hardware's square root and reciprocal (off by a step or two of fp32, far
-// below a code's own rounding and below p's in the update): with the exact
-// ones this kernel was bound by issue (83 instructions a value, 654 us for
-// 160 million values; see the table of cases for the time now).
-__device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, bool vec, const Hyper2& hp) {
-  const int64_t at = i0 + 8 * lane;
+// Where a block's values lie in a stage; p == 0: nowhere.
+struct Stage {
+  uint32_t p, g, m, v;
+};
+
+// A lane's eight values of a block: 4 lane + (0..3) and 128 + 4 lane + (0..3),
+// so that every access of a warp is one contiguous piece.
+__device__ __forceinline__ int value_of(int lane, int j) { return (j >> 2) * 128 + 4 * lane + (j & 3); }
+
+// The 8-bit step of the block at i0 (`src`: its stage, or 0 for plain
+// accesses; `read` is called once its values are in registers), in packed pairs, with the hardware's square root and reciprocal (off by a step
+// or two of fp32, far below a code's own rounding and below p's in the
+// update): with the exact ones this kernel was bound by issue (83
+// instructions a value, 654 us for 160 million values).
+template <typename Read>
+__device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, const Stage& src, const Hyper2& hp,
+                                      Read read) {
   const int64_t blk = i0 / kStateBlock;
-  const int valid = static_cast<int>(min(static_cast<int64_t>(8), max(static_cast<int64_t>(0), t.n - at)));
+  const int left = static_cast<int>(min(static_cast<int64_t>(kStateBlock), t.n - i0));
   const float ms = t.m_scales[blk], vs = t.v_scales[blk];
-  uint8_t* mc = static_cast<uint8_t*>(t.m) + at;
-  uint8_t* vc = static_cast<uint8_t*>(t.v) + at;
-  const bool wide = vec && valid == 8;
+  uint8_t* mc = static_cast<uint8_t*>(t.m) + i0;
+  uint8_t* vc = static_cast<uint8_t*>(t.v) + i0;
   float p[8], g[8];
   uint2 mq, vq;
-  if (wide) {
-    *reinterpret_cast<float4*>(g) = __ldcs(reinterpret_cast<const float4*>(t.grad + at));
-    *reinterpret_cast<float4*>(g + 4) = __ldcs(reinterpret_cast<const float4*>(t.grad + at + 4));
-    mq = *reinterpret_cast<const uint2*>(mc);
-    vq = *reinterpret_cast<const uint2*>(vc);
-    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(t.master + at);
-    *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(t.master + at + 4);
+  if (src.p != 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lds_f4(src.p + 512 * h + 16 * lane, p + 4 * h);
+      lds_f4(src.g + 512 * h + 16 * lane, g + 4 * h);
+    }
+    mq = make_uint2(lds_u1(src.m + 4 * lane), lds_u1(src.m + 128 + 4 * lane));
+    vq = make_uint2(lds_u1(src.v + 4 * lane), lds_u1(src.v + 128 + 4 * lane));
   } else {
     uint32_t mb[8], vb[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const bool ok = j < valid;
-      p[j] = ok ? t.master[at + j] : 0.0f;
-      g[j] = ok ? t.grad[at + j] : 0.0f;
-      mb[j] = ok ? mc[j] : 0u;
-      vb[j] = ok ? vc[j] : 0u;
+      const int c = value_of(lane, j);
+      const bool ok = c < left;
+      p[j] = ok ? t.master[i0 + c] : 0.0f;
+      g[j] = ok ? t.grad[i0 + c] : 0.0f;
+      mb[j] = ok ? mc[c] : 0u;
+      vb[j] = ok ? vc[c] : 0u;
     }
     mq = make_uint2(mb[0] | mb[1] << 8 | mb[2] << 16 | mb[3] << 24, mb[4] | mb[5] << 8 | mb[6] << 16 | mb[7] << 24);
     vq = make_uint2(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24, vb[4] | vb[5] << 8 | vb[6] << 16 | vb[7] << 24);
   }
+  read();
   const uint64_t ms2 = f2(ms, ms), vs2 = f2(vs, vs);
   float m[8], r[8];
   float am = 0.0f, av = 0.0f;
@@ -184,87 +203,175 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
     float* scale = lane == 0 ? t.m_scales : t.v_scales;
     scale[blk] = (lane == 0 ? am : av) / F;
   }
-  if (wide) {
-    *reinterpret_cast<float4*>(t.master + at) = *reinterpret_cast<const float4*>(p);
-    *reinterpret_cast<float4*>(t.master + at + 4) = *reinterpret_cast<const float4*>(p + 4);
-    *reinterpret_cast<uint2*>(mc) = mq;
-    *reinterpret_cast<uint2*>(vc) = vq;
-    if (t.param != nullptr)
-      *reinterpret_cast<uint4*>(t.param + at) = make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
-                                                           pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+  if (src.p != 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = i0 + 128 * h + 4 * lane;
+      *reinterpret_cast<float4*>(t.master + at) = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
+      reinterpret_cast<uint32_t*>(mc)[32 * h + lane] = h == 0 ? mq.x : mq.y;
+      reinterpret_cast<uint32_t*>(vc)[32 * h + lane] = h == 0 ? vq.x : vq.y;
+      if (t.param != nullptr)
+        *reinterpret_cast<uint2*>(t.param + at) =
+            make_uint2(pack_bf16x2(p[4 * h], p[4 * h + 1]), pack_bf16x2(p[4 * h + 2], p[4 * h + 3]));
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (j >= valid) continue;
-      t.master[at + j] = p[j];
-      mc[j] = static_cast<uint8_t>((j < 4 ? mq.x : mq.y) >> (8 * (j & 3)));
-      vc[j] = static_cast<uint8_t>((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
-      if (t.param != nullptr) t.param[at + j] = __float2bfloat16_rn(p[j]);
+      const int c = value_of(lane, j);
+      if (c >= left) continue;
+      t.master[i0 + c] = p[j];
+      mc[c] = static_cast<uint8_t>((j < 4 ? mq.x : mq.y) >> (8 * (j & 3)));
+      vc[c] = static_cast<uint8_t>((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
+      if (t.param != nullptr) t.param[i0 + c] = __float2bfloat16_rn(p[j]);
     }
   }
 }
 
-__device__ __forceinline__ void step32(const MultiTensor& t, int64_t at, bool vec, const AdamwHyper& hp) {
-  float* m = static_cast<float*>(t.m);
-  float* v = static_cast<float*>(t.v);
-  if (at >= t.n) return;
-  float root;
-  if (vec && at + 4 <= t.n) {
-    float4 p4 = *reinterpret_cast<const float4*>(t.master + at);
-    const float4 g4 = __ldcs(reinterpret_cast<const float4*>(t.grad + at));
-    float4 m4 = *reinterpret_cast<const float4*>(m + at);
-    float4 v4 = *reinterpret_cast<const float4*>(v + at);
-    p4.x = adamw_update(p4.x, g4.x, m4.x, v4.x, root, hp);
-    p4.y = adamw_update(p4.y, g4.y, m4.y, v4.y, root, hp);
-    p4.z = adamw_update(p4.z, g4.z, m4.z, v4.z, root, hp);
-    p4.w = adamw_update(p4.w, g4.w, m4.w, v4.w, root, hp);
-    *reinterpret_cast<float4*>(t.master + at) = p4;
-    *reinterpret_cast<float4*>(m + at) = m4;
-    *reinterpret_cast<float4*>(v + at) = v4;
-    if (t.param != nullptr)
-      *reinterpret_cast<uint2*>(t.param + at) = make_uint2(pack_bf16x2(p4.x, p4.y), pack_bf16x2(p4.z, p4.w));
-    return;
+// The same with fp32 states, in the arithmetic of qlora_adamw_step.
+template <typename Read>
+__device__ __forceinline__ void step32(const MultiTensor& t, int64_t i0, int lane, const Stage& src,
+                                       const AdamwHyper& hp, Read read) {
+  const int left = static_cast<int>(min(static_cast<int64_t>(kStateBlock), t.n - i0));
+  float* ms = static_cast<float*>(t.m) + i0;
+  float* vs = static_cast<float*>(t.v) + i0;
+  float p[8], g[8], m[8], v[8], root;
+  if (src.p != 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lds_f4(src.p + 512 * h + 16 * lane, p + 4 * h);
+      lds_f4(src.g + 512 * h + 16 * lane, g + 4 * h);
+      lds_f4(src.m + 512 * h + 16 * lane, m + 4 * h);
+      lds_f4(src.v + 512 * h + 16 * lane, v + 4 * h);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = value_of(lane, j);
+      const bool ok = c < left;
+      p[j] = ok ? t.master[i0 + c] : 0.0f;
+      g[j] = ok ? t.grad[i0 + c] : 0.0f;
+      m[j] = ok ? ms[c] : 0.0f;
+      v[j] = ok ? vs[c] : 0.0f;
+    }
   }
-  for (int64_t i = at; i < min(at + 4, t.n); ++i) {
-    float mi = m[i], vi = v[i];
-    const float p = adamw_update(t.master[i], t.grad[i], mi, vi, root, hp);
-    t.master[i] = p;
-    m[i] = mi;
-    v[i] = vi;
-    if (t.param != nullptr) t.param[i] = __float2bfloat16_rn(p);
+  read();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) p[j] = adamw_update(p[j], g[j], m[j], v[j], root, hp);
+  if (src.p != 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 128 * h + 4 * lane;
+      *reinterpret_cast<float4*>(t.master + i0 + c) = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
+      *reinterpret_cast<float4*>(ms + c) = make_float4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
+      *reinterpret_cast<float4*>(vs + c) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      if (t.param != nullptr)
+        *reinterpret_cast<uint2*>(t.param + i0 + c) =
+            make_uint2(pack_bf16x2(p[4 * h], p[4 * h + 1]), pack_bf16x2(p[4 * h + 2], p[4 * h + 3]));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = value_of(lane, j);
+      if (c >= left) continue;
+      t.master[i0 + c] = p[j];
+      ms[c] = m[j];
+      vs[c] = v[j];
+      if (t.param != nullptr) t.param[i0 + c] = __float2bfloat16_rn(p[j]);
+    }
   }
 }
 
+constexpr int kStages = 3;
+constexpr int stage_bytes(bool b8) { return kChunk * (b8 ? 10 : 16); }
+
 template <int CAP, bool BITS8>
-__global__ void __launch_bounds__(kThreads) k_adamw_multi(const __grid_constant__ Multi<CAP> a) {
+__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 2) k_adamw_multi(const __grid_constant__ Multi<CAP> a) {
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  __shared__ __align__(8) uint64_t s_bar[kStages];
+  constexpr uint32_t W = BITS8 ? 1 : 4;          // bytes of a state
+  constexpr uint32_t STAGE = stage_bytes(BITS8);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t ring = smem_u32(s_ring), bars = smem_u32(s_bar);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   grid_dependency_wait();
   grid_dependency_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Hyper2 hp2 = hyper2(a.hp);
-  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    // the last tensor whose first chunk is not past c
+  auto first = [&](int i) { return a.first[i] & 0x7FFFFFFF; };
+  const int stride = gridDim.x;
+  // cursors over this CTA's chunks: the one at work and the one to request
+  struct Cursor {
+    int chunk, t;
+  };
+  auto settle = [&](Cursor& c) {     // the last tensor whose first chunk is not past c.chunk
+    while (c.t + 1 < a.count && first(c.t + 1) <= c.chunk) ++c.t;
+  };
+  auto whole = [&](const Cursor& c) {   // a whole chunk of a tensor that takes wide accesses
+    return a.first[c.t] < 0 && static_cast<int64_t>(c.chunk - first(c.t) + 1) * kChunk <= a.t[c.t].n;
+  };
+  auto request = [&](const Cursor& c, int s) {   // one thread
+    if (c.chunk >= a.chunks || !whole(c)) return;
+    const MultiTensor& t = a.t[c.t];
+    const int64_t i0 = static_cast<int64_t>(c.chunk - first(c.t)) * kChunk;
+    const uint32_t dst = ring + s * STAGE, bar = bars + 8 * s;
+    mbar_arrive_expect_tx(bar, STAGE);
+    bulk_load(dst, t.master + i0, kChunk * 4, bar);
+    bulk_load(dst + kChunk * 4, t.grad + i0, kChunk * 4, bar);
+    bulk_load(dst + kChunk * 8, static_cast<const uint8_t*>(t.m) + i0 * W, kChunk * W, bar);
+    bulk_load(dst + kChunk * (8 + W), static_cast<const uint8_t*>(t.v) + i0 * W, kChunk * W, bar);
+  };
+  Cursor cur{static_cast<int>(blockIdx.x), 0}, ahead{};
+  {
     int lo = 0, hi = a.count - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((a.first[mid] & 0x7FFFFFFF) <= c)
+      if (first(mid) <= cur.chunk)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const MultiTensor& t = a.t[lo];
-    const bool vec = a.first[lo] < 0;
-    const int64_t i0 = static_cast<int64_t>(c - (a.first[lo] & 0x7FFFFFFF)) * kChunkValues;
-    if (BITS8) {
-#pragma unroll
-      for (int s = 0; s < kChunkValues / (kThreads * 8); ++s) {
-        const int64_t b0 = i0 + (s * (kThreads / 32) + warp) * kStateBlock;
-        if (b0 < t.n) step8(t, b0, lane, vec, hp2);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kChunkValues / (kThreads * 4); ++s)
-        step32(t, i0 + (s * kThreads + threadIdx.x) * 4, vec, a.hp);
+    cur.t = lo;
+  }
+  ahead = cur;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      settle(ahead);
+      request(ahead, s);
+      ahead.chunk += stride;   // at most 2^30 chunks: no overflow
     }
+  }
+  int s = 0;
+  uint32_t phases = 0;         // one bit a stage; it turns when the stage was filled
+  for (; cur.chunk < a.chunks; cur.chunk += stride) {
+    settle(cur);
+    const MultiTensor& t = a.t[cur.t];
+    const int64_t i0 = static_cast<int64_t>(cur.chunk - first(cur.t)) * kChunk + warp * kStateBlock;
+    Stage src{0, 0, 0, 0};
+    if (whole(cur)) {
+      if (!bulk_wait(bars + 8 * s, (phases >> s) & 1)) return;
+      phases ^= 1u << s;
+      const uint32_t at = ring + s * STAGE;
+      src = Stage{at + warp * 1024, at + kChunk * 4 + warp * 1024, at + kChunk * 8 + warp * (kStateBlock * W),
+                  at + kChunk * (8 + W) + warp * (kStateBlock * W)};
+    }
+    auto read = [&]() {
+      __syncthreads();         // every warp has read its part of the stage
+      if (threadIdx.x == 0) {
+        settle(ahead);
+        request(ahead, s);
+        ahead.chunk += stride;
+      }
+    };
+    if (i0 >= t.n)
+      read();
+    else if (BITS8)
+      step8(t, i0, lane, src, hp2, read);
+    else
+      step32(t, i0, lane, src, a.hp, read);
+    s = s + 1 == kStages ? 0 : s + 1;
   }
 }
 
@@ -282,15 +389,16 @@ int launch_multi(const qlora_adamw_tensor_t* t, const int* index, int count, con
     const qlora_adamw_tensor_t& s = t[index[i]];
     a.t[i] = MultiTensor{s.master, static_cast<__nv_bfloat16*>(s.param_bf16), s.grad, s.m, s.v,
                          s.m_scales, s.v_scales, s.n};
-    const unsigned state = BITS8 ? 8 : 16, copy = BITS8 ? 16 : 8;
-    const bool vec = aligned(s.master, 16) && aligned(s.grad, 16) && aligned(s.m, state) && aligned(s.v, state) &&
-                     aligned(s.param_bf16, copy);
+    const bool vec = aligned(s.master, 16) && aligned(s.grad, 16) && aligned(s.m, 16) && aligned(s.v, 16) &&
+                     aligned(s.param_bf16, 8);
     a.first[i] = static_cast<int32_t>(chunks) | (vec ? static_cast<int32_t>(0x80000000u) : 0);
-    chunks += cdiv(s.n, kChunkValues);
+    chunks += cdiv(s.n, kChunk);
   }
   a.chunks = static_cast<int32_t>(chunks);
-  const int grid = static_cast<int>(std::min<int64_t>(chunks, static_cast<int64_t>(sms) * 8));
-  return host::launch_pdl(k_adamw_multi<CAP, BITS8>, dim3(grid), dim3(kThreads), 0, st, 1, a);
+  // as many CTAs as the rings leave room for on an SM
+  const int64_t resident = static_cast<int64_t>(sms) * (BITS8 ? 3 : 2);
+  const int grid = static_cast<int>(std::min<int64_t>(chunks, resident));
+  return host::launch_pdl(k_adamw_multi<CAP, BITS8>, dim3(grid), dim3(kThreads), kStages * stage_bytes(BITS8), st, 1, a);
 }
 
 // Whether two of the ranges [at(i), at(i) + bytes(i)) of the listed tensors overlap.
@@ -310,6 +418,16 @@ bool overlap(const std::vector<int>& live, At at, Bytes bytes) {
 }
 
 }  // namespace
+
+cudaError_t set_adamw_attributes() {
+  const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(k_adamw_multi<kCapSmall, true>, a, kStages * stage_bytes(true));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_adamw_multi<kCapLarge, true>, a, kStages * stage_bytes(true));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_adamw_multi<kCapSmall, false>, a, kStages * stage_bytes(false));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_adamw_multi<kCapLarge, false>, a, kStages * stage_bytes(false));
+  return e;
+}
+
 }  // namespace qlora
 
 using namespace qlora;
@@ -329,7 +447,7 @@ extern "C" qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t* tensors,
     live.reserve(static_cast<size_t>(count));
     for (int64_t i = 0; i < count; ++i) {
       const qlora_adamw_tensor_t& t = tensors[i];
-      if (t.n < 0 || t.n > (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
+      if (t.n < 0 || t.n > (int64_t(1) << 38)) return QLORA_ERR_SHAPE;
       if (t.n == 0) continue;
       if (t.master == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr ||
           (b8 && (t.m_scales == nullptr || t.v_scales == nullptr)))
@@ -364,7 +482,7 @@ extern "C" qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t* tensors,
       size_t to = at;
       int64_t chunks = 0;
       while (to < live.size() && to - at < kCapLarge) {
-        const int64_t more = cdiv(tensors[live[to]].n, kChunkValues);
+        const int64_t more = cdiv(tensors[live[to]].n, kChunk);
         if (to > at && chunks + more > (int64_t(1) << 30)) break;
         chunks += more;
         ++to;
