@@ -18,7 +18,7 @@
 namespace qlora {
 
 qlora_status_t check_fp8_rows(const qlora_fp8_rows_t* r);
-int launch_quantize_rows(const void* x_bf16, const qlora_fp8_rows_t& out, cudaStream_t st);
+int launch_quantize_rows(const void* x_bf16, const qlora_fp8_rows_t& out, int sms, cudaStream_t st);
 
 namespace {
 
@@ -235,7 +235,7 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
     uint8_t* base = static_cast<uint8_t*>(ws);
     rows = qlora_fp8_rows_t{m, red, rup(red, 16), base + plan.codes, reinterpret_cast<float*>(base + plan.scales),
                             format, 0};
-    if ((s = static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, rows, st))) != QLORA_OK) return s;
+    if ((s = static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, rows, sms, st))) != QLORA_OK) return s;
   }
   const Product p{rows, q, out_bf16, m, cols, red, x8 == nullptr};
   return static_cast<qlora_status_t>(launch_product<BWD>(p, pairs, st));

@@ -53,6 +53,31 @@ struct NormBwd {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// a * b + c of the halves (lo or hi) of two bf16 pairs: the product is exact,
+// one rounding to fp32.
+__device__ __forceinline__ float fma_lo(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("{ .reg .b16 al, ah, bl, bh; mov.b32 {al, ah}, %1; mov.b32 {bl, bh}, %2; fma.rn.f32.bf16 %0, al, bl, %3; }"
+      : "=f"(d)
+      : "r"(a), "r"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float fma_hi(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("{ .reg .b16 al, ah, bl, bh; mov.b32 {al, ah}, %1; mov.b32 {bl, bh}, %2; fma.rn.f32.bf16 %0, ah, bh, %3; }"
+      : "=f"(d)
+      : "r"(a), "r"(b), "f"(c));
+  return d;
+}
+
+// bf16(a + b) of two pairs, the sum rounded once. (Rounding it to fp32 first
+// gives the same: a sum that fp32 does not hold is far from a tie of bf16.)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -167,13 +192,23 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, float* scales, int c0, i
   }
 }
 
-// Sum over the T threads of a row group (threadIdx.y); `red` has 32 floats a group.
+// Barrier of the threads of a row group (threadIdx.y < 15, whole warps).
+__device__ __forceinline__ void group_sync(int warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(warps * 32) : "memory");
+}
+
+// Sum over the T threads of a row group; `red` has as many floats as a group
+// has warps. OWN: the group meets at a barrier of its own, else the whole CTA.
+template <bool OWN>
 __device__ __forceinline__ float group_sum(float v, float* red, int warps) {
   v = warp_sum(v);
   if (warps == 1) return v;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) red[w] = v;
-  __syncthreads();
+  if (OWN)
+    group_sync(warps);
+  else
+    __syncthreads();
   return warp_sum(lane < warps ? red[lane] : 0.0f);
 }
 
@@ -183,10 +218,10 @@ constexpr size_t kBwdMaxSmem = 220 * 1024;
 enum NormOut : int { kOutBf16 = 0, kOutE4M3 = 1, kOutE5M2 = 2 };
 
 // NV chunks a warp, kept in registers; NV == 0: any width, h is read again
-// for the output (rows of over 32768 values).
+// for the output (rows of over 16384 values).
 // NORM false: the rows are only quantized (y = x).
 template <int NV, bool VEC, int OUT, bool NORM>
-__global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
+__global__ void __launch_bounds__(NV == 0 ? 1024 : 512) k_rows_fwd(NormFwd p) {
   __shared__ float s_red[32 * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -202,22 +237,17 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
   grid_dependency_wait();
   grid_dependency_trigger();
 
-  // both in packed pairs: this kernel is as much bound by issue as by HBM
+  // on bf16 pairs as they are: this kernel is as much bound by issue as by HBM
   auto add = [&](uint4 a, uint4 b) {
-    auto pair = [](uint32_t u, uint32_t v) {
-      uint32_t lo, hi;
-      f2_split(f2_add(f2(bf_lo(u), bf_hi(u)), f2(bf_lo(v), bf_hi(v))), lo, hi);
-      return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
-    };
-    return make_uint4(pair(a.x, b.x), pair(a.y, b.y), pair(a.z, b.z), pair(a.w, b.w));
+    return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
   };
-  uint64_t sum2 = 0;
+  float sum[2] = {0.0f, 0.0f};
   auto square = [&](uint4 t) {
     const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t v = f2(bf_lo(w[i]), bf_hi(w[i]));
-      sum2 = f2_fma(v, v, sum2);
+      sum[0] = fma_lo(w[i], w[i], sum[0]);
+      sum[1] = fma_hi(w[i], w[i], sum[1]);
     }
   };
   if constexpr (NV > 0) {
@@ -250,13 +280,9 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
   }
   float rstd = 1.0f;
   if (NORM) {
-    uint32_t lo, hi;
-    f2_split(sum2, lo, hi);
-    const float sum = group_sum(__uint_as_float(lo) + __uint_as_float(hi), s_red + 32 * threadIdx.y, warps);
-    rstd = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+    rstd = rsqrtf(fmaf(group_sum<false>(sum[0] + sum[1], s_red + 32 * threadIdx.y, warps), p.inv_d, p.eps));
     if (live && threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
   }
-  const uint64_t rstd2 = f2(rstd, rstd);
 #pragma unroll
   for (int v = 0; v < nstep; ++v) {
     const int c0 = v * step + warp * kChunk;
@@ -274,10 +300,8 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
       const uint32_t tw[4] = {t.x, t.y, t.z, t.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t lo, hi;
-        f2_split(f2_mul(f2_mul(f2(bf_lo(tw[i]), bf_hi(tw[i])), rstd2), f2(bf_lo(gw[i]), bf_hi(gw[i]))), lo, hi);
-        f[2 * i] = __uint_as_float(lo);
-        f[2 * i + 1] = __uint_as_float(hi);
+        f[2 * i] = fma_lo(tw[i], gw[i], 0.0f) * rstd;
+        f[2 * i + 1] = fma_hi(tw[i], gw[i], 0.0f) * rstd;
       }
     } else {
       unpack8(t, f);
@@ -289,22 +313,25 @@ __global__ void __launch_bounds__(1024) k_rows_fwd(NormFwd p) {
   }
 }
 
-// Gradients. A CTA of up to 512 threads holds groups of T threads, a row each.
-// A thread's columns are the same in every row, so its share of dgamma stays
-// in registers until the CTA's groups are added up through shared memory, in a
-// fixed order, into one partial row a CTA; k_dgamma adds the CTAs' rows.
+// Gradients. A CTA of up to 512 threads holds groups of T threads; each takes
+// rows of its own, at its own pace: where one waits for its row sum the others
+// compute (with one barrier for the CTA's two groups 4096 rows of 4096 took
+// 33.0 us). A thread's columns are the same in every row, so its share of
+// dgamma stays in registers until the CTA's groups are added up through shared
+// memory, in a fixed order, into one partial row a CTA; k_dgamma adds the
+// CTAs' rows.
 //
 // BULK (rows of whole 16-byte pieces that fit): the rows come through a ring
-// of p.stages stages in shared memory, filled by bulk copies, and are read
-// from there twice, for the row sum and for the output. The barrier of a
-// round's row sum shows that the round before is done with its stage; one
-// thread then refills it. Otherwise (odd widths, and NV == 0: wide rows, whose
+// of p.stages stages a group in shared memory, filled by bulk copies, and are
+// read from there twice, for the row sum and for the output. The barrier of a
+// row's sum shows that the group is done with the row before; one thread then
+// refills its stage. Otherwise (odd widths, and NV == 0: wide rows, whose
 // partial row is kept in global memory) plain loads.
 template <int NV, bool VEC, bool BULK>
 __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   extern __shared__ __align__(16) uint8_t s_dyn[];   // BULK: the stages; then d floats for the groups' dgamma
   __shared__ float s_red[2][16 * 16];
-  __shared__ __align__(8) uint64_t s_bar[kBwdMaxStages];
+  __shared__ __align__(8) uint64_t s_bar[16 * kBwdMaxStages];
   static_assert(!BULK || (VEC && NV > 0), "bulk copies are for whole rows in registers");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   constexpr int KEEP = NV > 0 ? NV : 1;
@@ -312,18 +339,19 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   const int step = warps * kChunk;
   const int nstep = NV > 0 ? NV : (width + step - 1) / step;
   const int groups = static_cast<int>(blockDim.y);
-  const bool one = threadIdx.x == 0 && threadIdx.y == 0;
+  const bool one = threadIdx.x == 0;     // of a group
   const uint32_t row_bytes = static_cast<uint32_t>(width) * 2;
   const int parts = p.dres != nullptr ? 3 : 2;
-  const uint32_t group_bytes = 3 * row_bytes, stage_bytes = groups * group_bytes;
-  const uint32_t dyn = smem_u32(s_dyn);
-  float acc[KEEP][8];
+  const uint32_t stage_bytes = 3 * row_bytes;
+  const uint32_t ring = smem_u32(s_dyn) + threadIdx.y * p.stages * stage_bytes;
+  const uint32_t bars = smem_u32(s_bar) + threadIdx.y * kBwdMaxStages * 8;
+  uint64_t acc[KEEP][4];
 #pragma unroll
   for (int v = 0; v < KEEP; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[v][j] = 0.0f;
+    for (int i = 0; i < 4; ++i) acc[v][i] = 0;
   if (BULK && one) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&s_bar[s]), 1);
+    for (int s = 0; s < p.stages; ++s) mbar_init(bars + 8 * s, 1);
     fence_mbar_init();
   }
   if (BULK) __syncthreads();
@@ -331,47 +359,38 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   grid_dependency_trigger();
   float* prow = p.part == nullptr ? nullptr : p.part + blockIdx.x * p.d;
 
-  // every group of the CTA runs the same number of rounds: the barrier of the
-  // row sum is the whole CTA's
   const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t rounds = (p.rows + stride - 1) / stride;
-  auto first_row = [&](int64_t i) { return (i * gridDim.x + blockIdx.x) * groups; };
-  auto fill = [&](int64_t i, int stage) {          // one thread: round i's rows
-    const int n = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(groups), p.rows - first_row(i))));
-    const uint32_t bar = smem_u32(&s_bar[stage]);
-    mbar_arrive_expect_tx(bar, n * parts * row_bytes);
-    for (int g = 0; g < n; ++g) {
-      const uint32_t dst = dyn + stage * stage_bytes + g * group_bytes;
-      const int64_t at = (first_row(i) + g) * p.d;
-      bulk_load(dst, p.dy + at, row_bytes, bar);
-      bulk_load(dst + row_bytes, p.h + at, row_bytes, bar);
-      if (parts == 3) bulk_load(dst + 2 * row_bytes, p.dres + at, row_bytes, bar);
-    }
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.y;
+  auto fill = [&](int64_t row, int stage) {          // one thread of the group
+    if (row >= p.rows) return;
+    const uint32_t bar = bars + 8 * stage, dst = ring + stage * stage_bytes;
+    mbar_arrive_expect_tx(bar, parts * row_bytes);
+    bulk_load(dst, p.dy + row * p.d, row_bytes, bar);
+    bulk_load(dst + row_bytes, p.h + row * p.d, row_bytes, bar);
+    if (parts == 3) bulk_load(dst + 2 * row_bytes, p.dres + row * p.d, row_bytes, bar);
   };
   if (BULK && one)
-    for (int i = 0; i < p.stages && i < rounds; ++i) fill(i, i);
+    for (int i = 0; i < p.stages; ++i) fill(row0 + i * stride, i);
   uint4 kg[KEEP];
   if constexpr (NV > 0) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) kg[v] = load8<VEC>(p.gamma, v * step + warp * kChunk, lane, width);
   }
 
-  int stage = 0;
+  int stage = 0, turn = 0;
   uint32_t phase = 0;
-  float next_rstd = first_row(0) + threadIdx.y < p.rows ? p.rstd[first_row(0) + threadIdx.y] : 0.0f;
-  for (int64_t i = 0; i < rounds; ++i) {
-    const int64_t row = first_row(i) + threadIdx.y;
-    const bool live = row < p.rows;
-    const int d = live ? width : 0;
+  float next_rstd = row0 < p.rows ? p.rstd[row0] : 0.0f;
+  for (int64_t row = row0; row < p.rows; row += stride) {
+    const int d = width;
     const __nv_bfloat16* dy = p.dy + row * p.d;
     const __nv_bfloat16* h = p.h + row * p.d;
-    const float rstd = next_rstd;       // fetched a round ahead
+    const float rstd = next_rstd;       // fetched a row ahead
     if (row + stride < p.rows) next_rstd = p.rstd[row + stride];
     uint4 kdy[KEEP], kh[KEEP], kres[KEEP];
     float dot = 0.0f;
-    const uint32_t src = dyn + stage * stage_bytes + threadIdx.y * group_bytes;
+    const uint32_t src = ring + stage * stage_bytes;
     if constexpr (BULK) {
-      if (!bulk_wait(smem_u32(&s_bar[stage]), phase)) return;
+      if (!bulk_wait(bars + 8 * stage, phase)) return;
     } else if constexpr (NV > 0) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -392,49 +411,57 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
         return load8<VEC>(part == 0 ? dy : part == 1 ? h : p.dres + row * p.d, c0, lane, d);
       }
     };
-    auto values = [&](int v, int c0, float (&a)[8], float (&b)[8], float (&g)[8]) {
-      unpack8(fetch(0, v, c0), a);
-      unpack8(fetch(1, v, c0), b);
-      unpack8(NV > 0 ? kg[NV > 0 ? v : 0] : load8<VEC>(p.gamma, c0, lane, width), g);
+    auto gain = [&](int v, int c0) -> uint4 {
+      return NV > 0 ? kg[NV > 0 ? v : 0] : load8<VEC>(p.gamma, c0, lane, width);
     };
 #pragma unroll
     for (int v = 0; v < nstep; ++v) {
-      float a[8], b[8], g[8];
-      values(v, v * step + warp * kChunk, a, b, g);
+      const int c0 = v * step + warp * kChunk;
+      const uint4 a = fetch(0, v, c0), b = fetch(1, v, c0), g = gain(v, c0);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dot = fmaf(a[j] * g[j], b[j], dot);
+      for (int i = 0; i < 4; ++i) {
+        dot = fmaf(fma_lo(aw[i], gw[i], 0.0f), bf_lo(bw[i]), dot);
+        dot = fmaf(fma_hi(aw[i], gw[i], 0.0f), bf_hi(bw[i]), dot);
+      }
     }
-    // two buffers in turn: a warp that is a round ahead does not overwrite sums still being read
-    dot = group_sum(dot, s_red[i & 1] + 16 * threadIdx.y, warps);
-    if (BULK) {
-      if (warps == 1) __syncthreads();     // with one warp a group the sum has no barrier
-      if (one && i > 0 && i - 1 + p.stages < rounds) fill(i - 1 + p.stages, stage == 0 ? p.stages - 1 : stage - 1);
-    }
-    const float c = dot * p.inv_d * rstd * rstd;
+    // two buffers in turn: a warp that is a row ahead does not overwrite sums still being read
+    dot = group_sum<true>(dot, s_red[turn] + warps * threadIdx.y, warps);
+    turn ^= 1;
+    if (BULK && one && row > row0) fill(row + (p.stages - 1) * stride, stage == 0 ? p.stages - 1 : stage - 1);
+    // dx = (dy g) rstd - h c + dres, dgamma += (dy rstd) h
+    const float c = dot * p.inv_d * rstd * rstd * rstd;
+    const uint64_t rstd2 = f2(rstd, rstd), c2 = f2(-c, -c);
 #pragma unroll
     for (int v = 0; v < nstep; ++v) {
       const int c0 = v * step + warp * kChunk;
-      float a[8], b[8], g[8], o[8];
-      values(v, c0, a, b, g);
+      const uint4 a = fetch(0, v, c0), b = fetch(1, v, c0), g = gain(v, c0);
+      const uint4 r = parts == 3 ? fetch(2, v, c0) : make_uint4(0, 0, 0, 0);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, gw[4] = {g.x, g.y, g.z, g.w},
+                     rw[4] = {r.x, r.y, r.z, r.w};
+      uint32_t o[4];
+      uint64_t grad[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (a[j] * g[j] - b[j] * c) * rstd;
-      if (parts == 3) {
-        float r[8];
-        unpack8(fetch(2, v, c0), r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += r[j];
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t b2 = f2(bf_lo(bw[i]), bf_hi(bw[i]));
+        const uint64_t ag = f2(fma_lo(aw[i], gw[i], 0.0f), fma_hi(aw[i], gw[i], 0.0f));
+        const uint64_t x2 = f2_fma(ag, rstd2, f2_fma(b2, c2, f2(bf_lo(rw[i]), bf_hi(rw[i]))));
+        uint32_t lo, hi;
+        f2_split(x2, lo, hi);
+        o[i] = pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+        grad[i] = f2_mul(f2_mul(f2(bf_lo(aw[i]), bf_hi(aw[i])), rstd2), b2);
       }
-      store8<VEC>(p.dx + row * p.d, c0, lane, d, pack8(o));
+      store8<VEC>(p.dx + row * p.d, c0, lane, d, make_uint4(o[0], o[1], o[2], o[3]));
       if (NV > 0) {
-        if (live) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[NV > 0 ? v : 0][j] = fmaf(a[j], b[j] * rstd, acc[NV > 0 ? v : 0][j]);
-        }
-      } else if (prow != nullptr && live) {
+        for (int i = 0; i < 4; ++i) acc[NV > 0 ? v : 0][i] = f2_add(acc[NV > 0 ? v : 0][i], grad[i]);
+      } else if (prow != nullptr) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int col = c0 + (VEC ? 8 * lane + j : lane + 32 * j);
-          if (col < d) prow[col] = fmaf(a[j], b[j] * rstd, i == 0 ? 0.0f : prow[col]);
+          uint32_t lo, hi;
+          f2_split(grad[j >> 1], lo, hi);
+          if (col < d) prow[col] = __uint_as_float(j & 1 ? hi : lo) + (row == row0 ? 0.0f : prow[col]);
         }
       }
     }
@@ -449,43 +476,61 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
     __syncthreads();                    // the stages are read: their memory takes the groups' sums
     for (int y = 0; y < groups; ++y) {
       if (static_cast<int>(threadIdx.y) == y) {
+        const bool last = y + 1 == groups;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+          const int c0 = v * step + warp * kChunk;
+          float own[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int col = v * step + warp * kChunk + (VEC ? 8 * lane + j : lane + 32 * j);
-            if (col < width) {
-              const float t = y == 0 ? acc[v][j] : s_part[col] + acc[v][j];
-              if (y + 1 < groups)
-                s_part[col] = t;
-              else
-                prow[col] = t;
+          for (int i = 0; i < 4; ++i) {
+            uint32_t lo, hi;
+            f2_split(acc[v][i], lo, hi);
+            own[2 * i] = __uint_as_float(lo);
+            own[2 * i + 1] = __uint_as_float(hi);
+          }
+          if (VEC) {
+            const int col = c0 + 8 * lane;
+            if (col >= width) continue;
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+              float4 t = make_float4(own[h], own[h + 1], own[h + 2], own[h + 3]);
+              if (y > 0) {
+                const float4 o = *reinterpret_cast<const float4*>(s_part + col + h);
+                t = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
+              }
+              *reinterpret_cast<float4*>((last ? prow : s_part) + col + h) = t;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int col = c0 + lane + 32 * j;
+              if (col < width) (last ? prow : s_part)[col] = (y > 0 ? s_part[col] : 0.0f) + own[j];
             }
           }
+        }
       }
       __syncthreads();
     }
   }
 }
 
-// dgamma[c] = sum over the partial rows, in a fixed order: 32 columns a CTA,
-// eight threads a column.
-__global__ void __launch_bounds__(256) k_dgamma(const float* __restrict__ part, int nrows, int64_t d, float* dgamma) {
-  __shared__ float s[8][33];
+// dgamma[c] = sum over the partial rows, in a fixed order: 32 columns a CTA, 32
+// threads a column, so that every load is in flight at once.
+__global__ void __launch_bounds__(1024) k_dgamma(const float* __restrict__ part, int nrows, int64_t d, float* dgamma) {
+  __shared__ float s[32][33];
   grid_dependency_wait();
   grid_dependency_trigger();
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
   float v = 0.0f;
   if (c < d) {
 #pragma unroll 8
-    for (int r = threadIdx.y; r < nrows; r += 8) v += part[r * d + c];
+    for (int r = threadIdx.y; r < nrows; r += 32) v += part[r * d + c];
   }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && c < d) {
-    for (int y = 1; y < 8; ++y) v += s[y][threadIdx.x];
-    dgamma[c] = v;
-  }
+  v = warp_sum(s[threadIdx.x][threadIdx.y]);      // warp y: column y
+  const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && out < d) dgamma[out] = v;
 }
 
 // ------------------------------------------------------------------ host
@@ -494,10 +539,15 @@ using host::cdiv;
 using host::rup;
 
 template <bool VEC, int OUT, bool NORM>
-int launch_rows(const NormFwd& p, cudaStream_t st) {
-  // two chunks a warp (16 values a thread) once the row is wide enough; short
-  // rows share a CTA of 256 threads
-  const int nv = p.d <= kChunk ? 1 : p.d <= 2 * 32 * kChunk ? 2 : p.d <= 4 * 32 * kChunk ? 4 : 0;
+int launch_rows(const NormFwd& p, int sms, cudaStream_t st) {
+  // up to four chunks a warp (32 values a thread), so that the sums and
+  // scales' fixed cost is shared by many values; short rows share a CTA of 256
+  // threads
+  // (4096 rows of 8192: 40.2 us, with two chunks 48.2) -- and two where few
+  // rows leave SMs idle, since latency counts then (1 row of 4096: 2.4 us, with four 3.0)
+  const int few = p.rows < 8 * static_cast<int64_t>(sms) ? 2 : 4;
+  const int nv = p.d <= kChunk ? 1 : p.d <= few * 16 * kChunk ? (p.d <= 8 * kChunk ? 2 : few)
+                                   : p.d <= 4 * 16 * kChunk ? 4 : 0;
   const int t = nv == 0 ? 1024 : static_cast<int>(cdiv(p.d, int64_t(kChunk) * nv)) * 32;
   const int r = t >= 256 ? 1 : 256 / t;
   const dim3 grid(static_cast<unsigned>(cdiv(p.rows, r))), block(t, r);
@@ -510,12 +560,12 @@ int launch_rows(const NormFwd& p, cudaStream_t st) {
 }
 
 template <int OUT, bool NORM>
-int launch_rows_vec(const NormFwd& p, cudaStream_t st) {
-  return p.d % 8 == 0 ? launch_rows<true, OUT, NORM>(p, st) : launch_rows<false, OUT, NORM>(p, st);
+int launch_rows_vec(const NormFwd& p, int sms, cudaStream_t st) {
+  return p.d % 8 == 0 ? launch_rows<true, OUT, NORM>(p, sms, st) : launch_rows<false, OUT, NORM>(p, sms, st);
 }
 
 // The backward's CTA: T threads a row, as many groups as 512 threads hold, and
-// as many bulk stages (three rows a group each) as fit, at least two.
+// as many bulk stages a group (three rows each) as fit, at least two.
 struct BwdPlan {
   int nv, t, r;
   int grid;
@@ -524,8 +574,9 @@ struct BwdPlan {
 
 BwdPlan plan_bwd(int64_t rows, int64_t d, int sms) {
   BwdPlan b;
-  // widths of 8192 to 16384 only through bulk stages: without them four chunks a warp do not fit the registers
-  b.nv = d <= kChunk ? 1 : d <= 2 * 16 * kChunk ? 2 : d <= 4 * 16 * kChunk && d % 8 == 0 ? 4 : 0;
+  // four chunks a warp only through bulk stages: without them the rows do not fit the registers
+  const int most = d % 8 == 0 ? 4 : 2;
+  b.nv = d <= kChunk ? 1 : d <= 2 * kChunk ? 2 : d <= most * 16 * kChunk ? most : 0;
   b.t = b.nv == 0 ? 512 : static_cast<int>(cdiv(d, int64_t(kChunk) * b.nv)) * 32;
   b.r = b.nv == 0 ? 1 : std::max(1, 512 / b.t);
   b.grid = static_cast<int>(std::min<int64_t>(sms, cdiv(rows, b.r)));
@@ -586,7 +637,7 @@ qlora_status_t check_fp8_rows(const qlora_fp8_rows_t* r) {
 }
 
 // Rows to 8 bits (arguments checked by the caller).
-int launch_quantize_rows(const void* x_bf16, const qlora_fp8_rows_t& out, cudaStream_t st) {
+int launch_quantize_rows(const void* x_bf16, const qlora_fp8_rows_t& out, int sms, cudaStream_t st) {
   NormFwd p{};
   p.x = static_cast<const __nv_bfloat16*>(x_bf16);
   p.codes = out.codes;
@@ -595,8 +646,8 @@ int launch_quantize_rows(const void* x_bf16, const qlora_fp8_rows_t& out, cudaSt
   p.d = out.cols;
   p.ld = out.ld;
   p.nblk = cdiv(out.cols, kFp8Block);
-  return out.format == QLORA_FP8_E5M2 ? launch_rows_vec<kOutE5M2, false>(p, st)
-                                      : launch_rows_vec<kOutE4M3, false>(p, st);
+  return out.format == QLORA_FP8_E5M2 ? launch_rows_vec<kOutE5M2, false>(p, sms, st)
+                                      : launch_rows_vec<kOutE4M3, false>(p, sms, st);
 }
 
 }  // namespace qlora
@@ -612,7 +663,7 @@ qlora_status_t qlora_quantize_fp8_rows(const void* x_bf16, const qlora_fp8_rows_
   if (!aligned(x_bf16, 16)) return QLORA_ERR_ALIGNMENT;
   int sms = 0;
   if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
-  return static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, *out, static_cast<cudaStream_t>(stream)));
+  return static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, *out, sms, static_cast<cudaStream_t>(stream)));
 }
 
 qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
@@ -647,13 +698,13 @@ qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, 
   p.eps = eps;
   p.inv_d = static_cast<float>(1.0 / static_cast<double>(d));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (y8 == nullptr) return static_cast<qlora_status_t>(launch_rows_vec<kOutBf16, true>(p, st));
+  if (y8 == nullptr) return static_cast<qlora_status_t>(launch_rows_vec<kOutBf16, true>(p, sms, st));
   p.codes = y8->codes;
   p.scales = y8->scales;
   p.ld = y8->ld;
   p.nblk = cdiv(d, kFp8Block);
-  return static_cast<qlora_status_t>(y8->format == QLORA_FP8_E5M2 ? launch_rows_vec<kOutE5M2, true>(p, st)
-                                                                  : launch_rows_vec<kOutE4M3, true>(p, st));
+  return static_cast<qlora_status_t>(y8->format == QLORA_FP8_E5M2 ? launch_rows_vec<kOutE5M2, true>(p, sms, st)
+                                                                  : launch_rows_vec<kOutE4M3, true>(p, sms, st));
 }
 
 size_t qlora_rmsnorm_workspace_bytes(int64_t rows, int64_t d) {
@@ -671,7 +722,7 @@ qlora_status_t qlora_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   qlora_status_t s;
   int sms = 0;
-  const dim3 rblock(32, 8), rgrid(static_cast<unsigned>(cdiv(d, 32)));
+  const dim3 rblock(32, 32), rgrid(static_cast<unsigned>(cdiv(d, 32)));
   if (rows == 0) {
     if (dgamma == nullptr) return QLORA_OK;
     if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;

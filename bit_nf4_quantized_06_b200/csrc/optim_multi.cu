@@ -281,11 +281,11 @@ __device__ __forceinline__ void step32(const MultiTensor& t, int64_t i0, int lan
   }
 }
 
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int stage_bytes(bool b8) { return kChunk * (b8 ? 10 : 16); }
 
 template <int CAP, bool BITS8>
-__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 2) k_adamw_multi(const __grid_constant__ Multi<CAP> a) {
+__global__ void __launch_bounds__(kThreads, 3) k_adamw_multi(const __grid_constant__ Multi<CAP> a) {
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ __align__(8) uint64_t s_bar[kStages];
   constexpr uint32_t W = BITS8 ? 1 : 4;          // bytes of a state
@@ -396,7 +396,7 @@ int launch_multi(const qlora_adamw_tensor_t* t, const int* index, int count, con
   }
   a.chunks = static_cast<int32_t>(chunks);
   // as many CTAs as the rings leave room for on an SM
-  const int64_t resident = static_cast<int64_t>(sms) * (BITS8 ? 3 : 2);
+  const int64_t resident = static_cast<int64_t>(sms) * 3;
   const int grid = static_cast<int>(std::min<int64_t>(chunks, resident));
   return host::launch_pdl(k_adamw_multi<CAP, BITS8>, dim3(grid), dim3(kThreads), kStages * stage_bytes(BITS8), st, 1, a);
 }
