@@ -22,13 +22,31 @@ struct Fp8Abort {
   volatile int* flag;       // shared memory, one a CTA
   unsigned int* status;     // the library's device status word
 };
-__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+// a few plain tries; a single instruction sequence, since what stands between
+// a barrier's phase and the work that waits for it counts in full
+__device__ __forceinline__ uint32_t fp8_tries(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "TRY_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 64;\n\t"
+      "@q bra TRY_%=;\n"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
+// one thread
+__device__ __forceinline__ bool fp8_wait_long(uint32_t bar, uint32_t parity, Fp8Abort a, unsigned code) {
   const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+  while (!fp8_tries(bar, parity)) {
     if (*a.flag) return false;
     if (globaltimer_ns() - t0 > QLORA_WAIT_LIMIT_NS) {
       atomicOr(a.status, code);
@@ -36,6 +54,19 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp
       return false;
     }
   }
+  return true;
+}
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
+  return fp8_tries(bar, parity) || fp8_wait_long(bar, parity, a, code);
+}
+
+// a whole warp: the same answer in every lane
+__device__ __forceinline__ bool fp8_warp_wait_long(uint32_t bar, uint32_t parity, Fp8Abort a, unsigned code) {
+  const bool ok = fp8_wait_long(bar, parity, a, code);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+__device__ __forceinline__ bool fp8_warp_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
+  return __all_sync(0xFFFFFFFFu, fp8_tries(bar, parity)) || fp8_warp_wait_long(bar, parity, a, code);
 }
 
 // Instruction descriptor for kind::f8f6f4: A e4m3 or e5m2, B e4m3, fp32 D.

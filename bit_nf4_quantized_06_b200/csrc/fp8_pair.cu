@@ -149,11 +149,9 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       bool ok = true;
       for (int tile = pair; ok && tile < ntiles; tile += npairs) {
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!fp8_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA) ||
-              !fp8_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA)) {
-            ok = false;
+          if (!(ok = fp8_warp_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA) &&
+                     fp8_warp_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)))
             break;
-          }
           tc_fence_after();
           if (elect_one()) {
             const uint32_t d = tmem_base + b * 256;
@@ -192,11 +190,7 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       const int ob = (tile / p.tiles_m) * 2 + half;          // this warp's weight block
       for (int k0 = 0; k0 < p.kblocks; k0 += kScaleChunk, ++ch) {
         const uint32_t slot = ring + (ch & 1) * (kScaleChunk * kScaleStride * 4) + kl * (kScaleStride * 4);
-        ok = fp8_wait(bar_se(ch & 1), ((ch >> 1) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER);
-        if (!warp_all(ok)) {
-          ok = false;
-          break;
-        }
+        if (!(ok = fp8_warp_wait(bar_se(ch & 1), ((ch >> 1) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER))) break;
         const int kb = k0 + kl;
         const bool live = kb < p.kblocks;
         const float* sx = p.sx + static_cast<int64_t>(row0 + rl) * p.xblk + kb;
@@ -239,11 +233,7 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
 #pragma unroll 1
       for (int kb = p.kblocks; kb > 0; --kb) {
         if (left == 0) {
-          ok = fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
-          if (!warp_all(ok)) {
-            ok = false;
-            break;
-          }
+          if (!(ok = fp8_warp_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
           left = min(kb, kScaleChunk);
           slot = c * (kScaleChunk * kScaleStride * 4);
         }
@@ -256,11 +246,7 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
           c ^= 1;
           if (c == 0) cph ^= 1;
         }
-        ok = fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
-        if (!warp_all(ok)) {
-          ok = false;
-          break;
-        }
+        if (!(ok = fp8_warp_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
         tc_fence_after();
         const uint32_t t = tbase + b * 256;
         uint32_t ra[16], rb[16];

@@ -149,11 +149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0, aph = 1;
     int last = -1;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!fp8_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA) ||
-          !fp8_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA)) {
-        ok = false;
-        break;
-      }
+      if (!(ok = fp8_warp_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA) &&
+                     fp8_warp_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)))
+            break;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t d = tmem_base + b * 128;
@@ -188,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cph = 1;
     for (int k0 = kb0; k0 < kb1; k0 += kScaleChunk) {
       const uint32_t slot = ring + (c * kScaleChunk + kl) * (kScaleStride * 4);
-      ok = fp8_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER);
-      if (!warp_all(ok)) break;
+      if (!(ok = fp8_warp_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER))) break;
       const int kb = k0 + kl;
       const bool live = kb < kb1;
       const float* sx = p.sx + static_cast<int64_t>(r0) * p.xblk + kb;
@@ -223,8 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int kb = kb1 - kb0; kb > 0; --kb) {
       if (left == 0) {
-        ok = fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
-        if (!warp_all(ok)) break;
+        if (!(ok = fp8_warp_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
         left = min(kb, kScaleChunk);
         slot = c * (kScaleChunk * kScaleStride * 4);
       }
@@ -237,8 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c ^= 1;
         if (c == 0) cph ^= 1;
       }
-      ok = fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
-      if (!warp_all(ok)) break;
+      if (!(ok = fp8_warp_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
       tc_fence_after();
       const uint32_t t = tbase + b * 128;
       uint32_t ra[16], rb[16], rc[16], rd[16];
