@@ -180,36 +180,44 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
   } else if (warp < 4) {
     // scales: chunks of eight reduction blocks, slot [block][128 rows, two
     // weight blocks]; read along the blocks (32 bytes a row), written along
-    // the rows, so that an epilogue warp's scales are one shared-memory line
+    // the rows, so that an epilogue warp's scales are one shared-memory line.
+    // A chunk is requested while the one before is at work: its loads wait in
+    // registers for the slot (requested only once the slot was free, they held
+    // the epilogue up by 320 to 700 cycles a block).
     const int half = warp - 2;                  // rows [64 half, 64 half + 64)
     const int kl = lane & 7, rl = lane >> 3;
-    int ch = 0;
-    bool ok = true;
-    for (int tile = pair; ok && tile < ntiles; tile += npairs) {
-      const int row0 = (tile % p.tiles_m) * 256 + 128 * rank + 64 * half;
+    float v[16], w = 0.0f;
+    auto request = [&](int tile, int k0) {
+      const int row0 = (tile % p.tiles_m) * 256 + 128 * rank + 64 * half + rl;
       const int ob = (tile / p.tiles_m) * 2 + half;          // this warp's weight block
-      for (int k0 = 0; k0 < p.kblocks; k0 += kScaleChunk, ++ch) {
-        const uint32_t slot = ring + (ch & 1) * (kScaleChunk * kScaleStride * 4) + kl * (kScaleStride * 4);
-        if (!(ok = fp8_warp_wait(bar_se(ch & 1), ((ch >> 1) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER))) break;
-        const int kb = k0 + kl;
-        const bool live = kb < p.kblocks;
-        const float* sx = p.sx + static_cast<int64_t>(row0 + rl) * p.xblk + kb;
-#pragma unroll 1
-        for (int i = 0; i < 64; i += 32) {
-          float v[8];
+      const int kb = k0 + kl;
+      const bool live = tile < ntiles && kb < p.kblocks;
+      const float* sx = p.sx + static_cast<int64_t>(row0) * p.xblk + kb;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)     // a row or block past the end has scale zero
-            v[j] = (live && row0 + rl + i + 4 * j < p.m) ? __ldg(sx + (i + 4 * j) * p.xblk) : 0.0f;
+      for (int j = 0; j < 16; ++j)      // a row or block past the end has scale zero
+        v[j] = (live && row0 + 4 * j < p.m) ? __ldg(sx + 4 * j * p.xblk) : 0.0f;
+      w = (live && rl == 0 && ob * 128 < p.cols) ? __ldg(p.sw + ob * p.sw_out + kb * p.sw_red) : 0.0f;
+    };
+    int c = 0;
+    uint32_t cph = 1;
+    int tile = pair, k0 = 0;
+    request(tile, k0);
+    while (tile < ntiles) {
+      const uint32_t slot = ring + (c * kScaleChunk + kl) * (kScaleStride * 4);
+      if (!fp8_warp_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER)) break;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sts32(slot + 4 * (64 * half + rl + i + 4 * j), __float_as_uint(v[j]));
-        }
-        if (rl == 0) {
-          const float w = (live && ob * 128 < p.cols) ? __ldg(p.sw + ob * p.sw_out + kb * p.sw_red) : 0.0f;
-          sts32(slot + 4 * (128 + half), __float_as_uint(w));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sf(ch & 1));
+      for (int j = 0; j < 16; ++j) sts32(slot + 4 * (64 * half + rl + 4 * j), __float_as_uint(v[j]));
+      if (rl == 0) sts32(slot + 4 * (128 + half), __float_as_uint(w));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sf(c));
+      c ^= 1;
+      if (c == 0) cph ^= 1;
+      k0 += kScaleChunk;
+      if (k0 >= p.kblocks) {
+        k0 = 0;
+        tile += npairs;
       }
+      request(tile, k0);
     }
   } else {
     setmaxnreg_inc<kFp8PairEpiRegs>();
@@ -295,15 +303,39 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
             if (col0 + 32 * c4 < p.cols) tma_store_2d(&tm_out, box + c4 * 2048, col0 + 32 * c4, row0);
           bulk_commit();
         }
-      } else if (row0 + lane < p.m) {
-        __nv_bfloat16* y = p.y + static_cast<int64_t>(row0 + lane) * p.cols + col0;
+      } else {
+        // rows that are not 16-byte aligned: through the same memory (16-byte
+        // pieces, the row's low bits exchanged into the piece's), then a row a
+        // warp, so that a store is one contiguous piece (a row a lane took 15 us
+        // more for one tile)
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          uint32_t lo, hi;
-          f2_split(acc[i], lo, hi);
-          if (col0 + 2 * i < p.cols) y[2 * i] = __float2bfloat16_rn(__uint_as_float(lo));
-          if (col0 + 2 * i + 1 < p.cols) y[2 * i + 1] = __float2bfloat16_rn(__uint_as_float(hi));
+        for (int v = 0; v < 16; ++v) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t lo, hi;
+            f2_split(acc[4 * v + e], lo, hi);
+            pk[e] = pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+          }
+          sts128(box + lane * 256 + ((v ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
         }
+        __syncwarp();
+        const int rows = min(32, p.m - row0), cols = min(128, p.cols - col0);
+        for (int r = 0; r < rows; ++r) {
+          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + static_cast<int64_t>(row0 + r) * p.cols + col0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = 64 * h + 2 * lane;
+            const uint32_t w = lds32(box + r * 256 + (((col >> 3) ^ (r & 7)) << 4) + 2 * (col & 7));
+            if (col + 1 < cols && p.cols % 2 == 0) {
+              *reinterpret_cast<uint32_t*>(y + col) = w;
+            } else {
+              if (col < cols) y[col] = static_cast<uint16_t>(w);
+              if (col + 1 < cols) y[col + 1] = static_cast<uint16_t>(w >> 16);
+            }
+          }
+        }
+        __syncwarp();                          // the box is read before the next tile fills it
       }
     }
     if (lane == 0) bulk_wait_all();   // stores complete before the CTA's shared memory goes away
