@@ -124,11 +124,11 @@ struct Product {
 
 // The tile shape and the split, by an estimate of the time in microseconds.
 // Measured on B200 with rows already in 8 bits:
-//   pair kernel   5 + waves (1.5 + 0.55 blocks): 4096^3 70.7, 512 rows x 4096 x 4096 19.6
-//   split kernel  waves (4.6 + S (0.1 + 0.002 rows) + 0.32 ceil(blocks / S)), a wave being the
+//   pair kernel   5 + waves (1.5 + 0.40 blocks): 512 rows x 4096 x 4096 17.8, 1024 rows 18.9, 2048 rows 33.6
+//   split kernel  waves (4.6 + S (0.1 + 0.002 rows) + 0.28 ceil(blocks / S)), a wave being the
 //                 clusters of S CTAs that are resident at once:
-//                 4096 x 4096 weight, 1 row: 12.6 (S = 1), 8.0 (2), 6.4 (4), 14.4 (8, two waves);
-//                 128 rows: 14.6, 10.4, 9.0, 23.1; 512 rows, S = 1: 15.2 (pair 19.6); 1024 rows: 30.5 (pair 20.7)
+//                 4096 x 4096 weight, 1 row: 11.8 (S = 1), 7.8 (2), 6.3 (4), 13.9 (8, two waves);
+//                 128 rows: 13.8, 10.1, 8.7, 21.9; 512 rows, S = 1: 14.8; 1024 rows: 29.0
 struct Choice {
   bool pair;
   int splits;
@@ -138,7 +138,7 @@ Choice choose(int64_t m, int64_t cols, int64_t kblocks, int dev, int pairs) {
   const double blocks = static_cast<double>(kblocks);
   const int64_t pair_waves = cdiv(cdiv(m, 256) * cdiv(cols, 256), pairs);
   Choice best{true, 1};
-  double best_cost = 5.0 + static_cast<double>(pair_waves) * (1.5 + 0.55 * blocks);
+  double best_cost = 5.0 + static_cast<double>(pair_waves) * (1.5 + 0.40 * blocks);
   const int64_t tiles = cdiv(m, 128) * cdiv(cols, 128);
   const double rows = static_cast<double>(std::min<int64_t>(m, 128));
   for (int s = 1; s <= kFp8MaxSplits && s <= kblocks && tiles * s < (int64_t(1) << 30); ++s) {
@@ -146,7 +146,7 @@ Choice choose(int64_t m, int64_t cols, int64_t kblocks, int dev, int pairs) {
     if (resident < 1) continue;
     const double waves = static_cast<double>(cdiv(tiles, resident));
     const double cost =
-        waves * (4.6 + (s > 1 ? s * (0.1 + 0.002 * rows) : 0.0) + 0.32 * static_cast<double>(cdiv(kblocks, s)));
+        waves * (4.6 + (s > 1 ? s * (0.1 + 0.002 * rows) : 0.0) + 0.28 * static_cast<double>(cdiv(kblocks, s)));
     if (cost < best_cost) {
       best_cost = cost;
       best = Choice{false, s};

@@ -14,39 +14,44 @@
 
 namespace qlora {
 
-// Bounded wait for the phase with the given parity: plain tries first (the
-// timer of the bound is slow to read next to a step of this pipeline), then
-// tries under the library's time limit. On timeout, or when another role has
-// given up, false; a timeout sets `code` in the device status word.
+// Waits. On timeout (two seconds), or when another role has given up, false; a
+// timeout sets `code` in the device status word.
 struct Fp8Abort {
   volatile int* flag;       // shared memory, one a CTA
   unsigned int* status;     // the library's device status word
 };
-// a few plain tries; a single instruction sequence, since what stands between
-// a barrier's phase and the work that waits for it counts in full
-__device__ __forceinline__ uint32_t fp8_tries(uint32_t bar, uint32_t parity) {
+
+// A token: whether the phase is over, without waiting for it.
+//
+// What stands between a barrier's phase and the work that waits for it counts
+// in full here (a reduction block is 256 or 512 cycles of tensor core), and a
+// wait of the usual form costs 100 to 200 cycles even where the phase is long
+// over: the try's latency, its loop and the vote that makes the answer the
+// same in every lane. So a role first takes a token, looks at it after other
+// work, and waits only where it failed; and warps do not vote: a wait that
+// gives up just goes on (the flag then ends every later wait at its first try,
+// and results are void), so lanes need not agree.
+__device__ __forceinline__ bool fp8_token(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n"
-      "TRY_%=:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 64;\n\t"
-      "@q bra TRY_%=;\n"
-      "DONE_%=:\n\t"
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
-  return ok;
+  return ok != 0;
 }
 
-// one thread
-__device__ __forceinline__ bool fp8_wait_long(uint32_t bar, uint32_t parity, Fp8Abort a, unsigned code) {
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*a.flag) return false;
+  }
   const uint64_t t0 = globaltimer_ns();
-  while (!fp8_tries(bar, parity)) {
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (*a.flag) return false;
     if (globaltimer_ns() - t0 > QLORA_WAIT_LIMIT_NS) {
       atomicOr(a.status, code);
@@ -54,19 +59,6 @@ __device__ __forceinline__ bool fp8_wait_long(uint32_t bar, uint32_t parity, Fp8
       return false;
     }
   }
-  return true;
-}
-__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
-  return fp8_tries(bar, parity) || fp8_wait_long(bar, parity, a, code);
-}
-
-// a whole warp: the same answer in every lane
-__device__ __forceinline__ bool fp8_warp_wait_long(uint32_t bar, uint32_t parity, Fp8Abort a, unsigned code) {
-  const bool ok = fp8_wait_long(bar, parity, a, code);
-  return __all_sync(0xFFFFFFFFu, ok);
-}
-__device__ __forceinline__ bool fp8_warp_wait(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
-  return __all_sync(0xFFFFFFFFu, fp8_tries(bar, parity)) || fp8_warp_wait_long(bar, parity, a, code);
 }
 
 // Instruction descriptor for kind::f8f6f4: A e4m3 or e5m2, B e4m3, fp32 D.

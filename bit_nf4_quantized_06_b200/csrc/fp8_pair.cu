@@ -138,45 +138,38 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       for (int j = max(0, it - STAGES); j < it; ++j) drain_wait(bar_empty(j % STAGES), (j / STAGES) & 1);
     }
   } else if (warp == 1) {
-    // the whole warp runs the loop, so that everything the MMAs take is uniform
-    // over the warp; one elected lane issues
-    if (leader) {
+    if (leader && elect_one()) {
       const uint32_t idesc = idesc_fp8(256, 256, p.a_format, W_MN);
       const uint64_t dx0 = smem_desc_sw128(base, 16, 1024);
       const uint64_t dw0 = W_MN ? smem_desc_sw128(base + HALF, HALF, 1024) : smem_desc_sw128(base + HALF, 16, 1024);
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 1;     // parities of the stage and of the buffer
-      bool ok = true;
-      for (int tile = pair; ok && tile < ntiles; tile += npairs) {
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!(ok = fp8_warp_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA) &&
-                     fp8_warp_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)))
-            break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t d = tmem_base + b * 256;
-            const uint64_t dx = dx0 + s * (STAGE_BYTES >> 4), dw = dw0 + s * (STAGE_BYTES >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)   // 32 of the reduction each
-              tc_mma_fp8_pair(d, dx + kk * 2, dw + kk * (W_MN ? 256 : 2), idesc, kk > 0 ? 1u : 0u);
-            tc_commit_both(bar_accf(b));
-            tc_commit_both(bar_empty(s));
-          }
-          __syncwarp();
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1;
-          }
-          b ^= 1;
-          if (b == 0) aph ^= 1;
+      bool full = false, free = false;
+      const int64_t blocks = static_cast<int64_t>((ntiles - pair + npairs - 1) / npairs) * p.kblocks;
+      for (int64_t i = 0; i < blocks; ++i) {
+        if (!full && !fp8_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
+        if (!free && !fp8_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + b * 256, accf = bar_accf(b), empty = bar_empty(s);
+        const uint64_t dx = dx0 + s * (STAGE_BYTES >> 4), dw = dw0 + s * (STAGE_BYTES >> 4);
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
         }
+        b ^= 1;
+        if (b == 0) aph ^= 1;
+        full = fp8_token(bar_full(s), ph);
+        free = fp8_token(bar_acce(b), aph);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)   // 32 of the reduction each
+          tc_mma_fp8_pair(d, dx + kk * 2, dw + kk * (W_MN ? 256 : 2), idesc, kk > 0 ? 1u : 0u);
+        tc_commit_both(accf);
+        tc_commit_both(empty);
       }
-      if (elect_one()) {
-        tc_commit_pair(bar_fin);
-        drain_wait(bar_fin, 0);
-      }
-      __syncwarp();
+      tc_commit_pair(bar_fin);
+      drain_wait(bar_fin, 0);
     }
+    __syncwarp();
   } else if (warp < 4) {
     // scales: chunks of eight reduction blocks, slot [block][128 rows, two
     // weight blocks]; read along the blocks (32 bytes a row), written along
@@ -202,9 +195,10 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
     uint32_t cph = 1;
     int tile = pair, k0 = 0;
     request(tile, k0);
-    while (tile < ntiles) {
+    while (tile < ntiles && !__any_sync(0xFFFFFFFFu, *abort_flag)) {
       const uint32_t slot = ring + (c * kScaleChunk + kl) * (kScaleStride * 4);
-      if (!fp8_warp_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER)) break;
+      if (!fp8_token(bar_se(c), cph)) fp8_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER);
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < 16; ++j) sts32(slot + 4 * (64 * half + rl + 4 * j), __float_as_uint(v[j]));
       if (rl == 0) sts32(slot + 4 * (128 + half), __float_as_uint(w));
@@ -229,8 +223,9 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
     const uint32_t ring_x = ring + 4 * (32 * quarter + lane), ring_w = ring + 4 * (128 + half);
     int b = 0, c = 0;              // accumulator buffer, scale chunk buffer
     uint32_t bph = 0, cph = 0;     // their parities
-    bool ok = true;
-    for (int tile = pair; ok && tile < ntiles; tile += npairs) {
+    bool ready = false;            // token of bar_accf(b)
+    for (int tile = pair; tile < ntiles; tile += npairs) {
+      if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
       const int row0 = (tile % p.tiles_m) * 256 + 128 * rank + 32 * quarter;
       const int col0 = (tile / p.tiles_m) * 256 + 128 * half;
       uint64_t acc[64];
@@ -241,7 +236,8 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
 #pragma unroll 1
       for (int kb = p.kblocks; kb > 0; --kb) {
         if (left == 0) {
-          if (!(ok = fp8_warp_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
+          if (!fp8_token(bar_sf(c), cph)) fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
+          __syncwarp();
           left = min(kb, kScaleChunk);
           slot = c * (kScaleChunk * kScaleStride * 4);
         }
@@ -254,9 +250,13 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
           c ^= 1;
           if (c == 0) cph ^= 1;
         }
-        if (!(ok = fp8_warp_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
+        if (!ready) fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
+        __syncwarp();
         tc_fence_after();
         const uint32_t t = tbase + b * 256;
+        const uint32_t acce = acce_even0 + 8u * b;
+        b ^= 1;
+        if (b == 0) bph ^= 1;
         uint32_t ra[16], rb[16];
         tmem_ld_32x32b_x16(t, ra);
         tmem_ld_32x32b_x16(t + 16, rb);
@@ -266,17 +266,15 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
           if (i == 6) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acce_even0 + 8u * b);
+            if (lane == 0) mbar_arrive_cluster(acce);
+            ready = fp8_token(bar_accf(b), bph);
           }
           promote16(acc + 8 * i, ra, s2);
           if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 2), ra);
           promote16(acc + 8 * (i + 1), rb, s2);
           if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 3), rb);
         }
-        b ^= 1;
-        if (b == 0) bph ^= 1;
       }
-      if (!ok) break;
       if (p.tma_out) {
         if (lane == 0) bulk_wait_read_all();   // the previous tile's stores have read the boxes
         __syncwarp();

@@ -145,68 +145,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_fp8(128, 128, p.a_format, W_MN);
     const uint64_t dx0 = smem_desc_sw128(base, 16, 1024);
     const uint64_t dw0 = W_MN ? smem_desc_sw128(base + HALF, HALF, 1024) : smem_desc_sw128(base + HALF, 16, 1024);
-    int s = 0, b = 0;
-    uint32_t ph = 0, aph = 1;
-    int last = -1;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!(ok = fp8_warp_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA) &&
-                     fp8_warp_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)))
-            break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tmem_base + b * 128;
+    if (elect_one()) {
+      int s = 0, b = 0, last = -1;
+      uint32_t ph = 0, aph = 1, last_ph = 0;
+      bool full = false, free = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!full && !fp8_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
+        if (!free && !fp8_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + b * 128, accf = bar_accf(b), empty = bar_empty(s);
         const uint64_t dx = dx0 + s * (STAGE_BYTES >> 4), dw = dw0 + s * (STAGE_BYTES >> 4);
+        last = s;
+        last_ph = ph;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+        if (++b == kBufs) {
+          b = 0;
+          aph ^= 1;
+        }
+        full = fp8_token(bar_full(s), ph);
+        free = fp8_token(bar_acce(b), aph);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           tc_mma_fp8(d, dx + kk * 2, dw + kk * (W_MN ? 256 : 2), idesc, kk > 0 ? 1u : 0u);
-        tc_commit(bar_accf(b));
-        tc_commit(bar_empty(s));
+        tc_commit(accf);
+        tc_commit(empty);
       }
-      __syncwarp();
-      last = s;
-      if (++s == kStages) {
-        s = 0;
-        ph ^= 1;
-      }
-      if (++b == kBufs) {
-        b = 0;
-        aph ^= 1;
-      }
+      // the last stage issued is free: no MMA of this CTA is in flight any more
+      if (last >= 0) drain_wait(bar_empty(last), last_ph);
     }
-    // the last stage issued is free: no MMA of this CTA is in flight any more
-    if (last >= 0) drain_wait(bar_empty(last), s == 0 ? ph ^ 1 : ph);
+    __syncwarp();
   } else if (warp < 4) {
-    // scales: see the pair kernel
+    // scales: as in the pair kernel, a chunk requested while the one before is at work
     grid_dependency_wait();
     const int half = warp - 2;
     const int kl = lane & 7, rl = lane >> 3;
     const int r0 = row0 + 64 * half + rl;
     const int ob = col0 >> 7;
-    int c = 0;
-    uint32_t cph = 1;
-    for (int k0 = kb0; k0 < kb1; k0 += kScaleChunk) {
-      const uint32_t slot = ring + (c * kScaleChunk + kl) * (kScaleStride * 4);
-      if (!(ok = fp8_warp_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER))) break;
+    float v[16], w = 0.0f;
+    auto request = [&](int k0) {
       const int kb = k0 + kl;
-      const bool live = kb < kb1;
+      const bool in = kb < kb1;
       const float* sx = p.sx + static_cast<int64_t>(r0) * p.xblk + kb;
 #pragma unroll
-      for (int i = 0; i < 64; i += 32) {
-        if (64 * half + i >= rows) break;      // rows past the end are not stored
-        float v[8];
+      for (int j = 0; j < 16; ++j) v[j] = (in && r0 + 4 * j < p.m) ? __ldg(sx + 4 * j * p.xblk) : 0.0f;
+      w = (in && half == 0 && rl == 0) ? __ldg(p.sw + ob * p.sw_out + kb * p.sw_red) : 0.0f;
+    };
+    int c = 0;
+    uint32_t cph = 1;
+    request(kb0);
+    for (int k0 = kb0; k0 < kb1; k0 += kScaleChunk) {
+      const uint32_t slot = ring + (c * kScaleChunk + kl) * (kScaleStride * 4);
+      if (!fp8_token(bar_se(c), cph)) fp8_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER);
+      __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (live && r0 + i + 4 * j < p.m) ? __ldg(sx + (i + 4 * j) * p.xblk) : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sts32(slot + 4 * (64 * half + rl + i + 4 * j), __float_as_uint(v[j]));
-      }
-      if (half == 0 && rl == 0) {
-        const float w = live ? __ldg(p.sw + ob * p.sw_out + kb * p.sw_red) : 0.0f;
-        sts32(slot + 4 * 128, __float_as_uint(w));
-      }
+      for (int j = 0; j < 16; ++j) sts32(slot + 4 * (64 * half + rl + 4 * j), __float_as_uint(v[j]));
+      if (half == 0 && rl == 0) sts32(slot + 4 * 128, __float_as_uint(w));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sf(c));
       c ^= 1;
       if (c == 0) cph ^= 1;
+      request(k0 + kScaleChunk);
     }
   } else {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
@@ -217,10 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 32; ++i) acc[i] = 0;
     int b = 0, c = 0, left = 0;
     uint32_t bph = 0, cph = 0, slot = 0;
+    bool ready = false;              // token of bar_accf(b)
 #pragma unroll 1
     for (int kb = kb1 - kb0; kb > 0; --kb) {
       if (left == 0) {
-        if (!(ok = fp8_warp_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
+        if (!fp8_token(bar_sf(c), cph)) fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
+        __syncwarp();
         left = min(kb, kScaleChunk);
         slot = c * (kScaleChunk * kScaleStride * 4);
       }
@@ -233,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         c ^= 1;
         if (c == 0) cph ^= 1;
       }
-      if (!(ok = fp8_warp_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI))) break;
+      if (!ready) fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
+      __syncwarp();
       tc_fence_after();
       const uint32_t t = tbase + b * 128;
       uint32_t ra[16], rb[16], rc[16], rd[16];
@@ -245,20 +249,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acce(b));
-      promote16(acc, ra, s2);
-      promote16(acc + 8, rb, s2);
-      promote16(acc + 16, rc, s2);
-      promote16(acc + 24, rd, s2);
       if (++b == kBufs) {
         b = 0;
         bph ^= 1;
       }
+      ready = fp8_token(bar_accf(b), bph);
+      promote16(acc, ra, s2);
+      promote16(acc + 8, rb, s2);
+      promote16(acc + 16, rc, s2);
+      promote16(acc + 24, rd, s2);
     }
     // All of this CTA's MMAs are done and its loads consumed: the sums go
     // where the stages were.
-    ok = __all_sync(0xFFFFFFFFu, ok);
     const int r = 32 * quarter + lane;
-    if (ok && r < rows) {
+    if (r < rows) {
       const uint32_t dst = base + (r * kPartStride + 64 * half) * 4;
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
