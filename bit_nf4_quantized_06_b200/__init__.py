@@ -621,8 +621,9 @@ def _fp8_product(call, where, q, x, fmt, cols_in, cols_out, out, ws):
         _want(_is(out, torch.bfloat16, (m, cols_out), dev), where, f"the output must be contiguous bf16 [m, {cols_out}]")
     if ws is not None:
         _want(ws.get_device() == dev and ws.is_contiguous(), where, "the workspace must be contiguous, on the weight's device")
-    elif rows is None:           # rows already in 8 bits need none
-        ws = torch.empty(lib.qlora_fp8_workspace_bytes(m, q.n_out, q.k_in), dtype=torch.uint8, device=src.device)
+    elif rows is None:           # rows already in 8 bits need none, nor do a few
+        need = lib.qlora_fp8_workspace_bytes(m, q.n_out, q.k_in)
+        ws = torch.empty(need, dtype=torch.uint8, device=src.device) if need else None
     at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     args = (q.struct(), None if rows is not None else x.data_ptr(), rows) + (() if fmt is None else (int(fmt),))
     _check(call(*args, m, out.data_ptr(), at, size, _raw_stream(dev)), where)

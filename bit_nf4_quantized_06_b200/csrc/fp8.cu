@@ -116,6 +116,7 @@ qlora_status_t check_weight(const qlora_fp8_t* q) {
 
 struct Product {
   qlora_fp8_rows_t x;      // [m x red]
+  const void* x16;         // bf16 rows to quantize within the product, or null
   const qlora_fp8_t* q;
   void* y;                 // [m x cols]
   int64_t m, cols, red;    // red: K forward, N backward
@@ -156,9 +157,7 @@ Choice choose(int64_t m, int64_t cols, int64_t kblocks, int dev, int pairs) {
 }
 
 template <bool BWD>
-int launch_product(const Product& p, int pairs, cudaStream_t st) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_CUDA;
+int launch_product(const Product& p, int dev, int pairs, cudaStream_t st) {
   const qlora_fp8_t& q = *p.q;
   const int64_t nbk = cdiv(q.k_in, kFp8Block);
   Fp8Gemm g{};
@@ -176,6 +175,8 @@ int launch_product(const Product& p, int pairs, cudaStream_t st) {
   g.tma_out = p.cols % 8 == 0;
   if (cdiv(p.m, 256) * cdiv(p.cols, 256) > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;   // tile numbers are 32-bit
   const Choice c = choose(p.m, p.cols, g.xblk, dev, pairs);
+  g.x16 = static_cast<const __nv_bfloat16*>(p.x16);
+  g.red = p.red;
   const int tile = c.pair ? 256 : 128;
   g.tiles_m = static_cast<int32_t>(cdiv(p.m, tile));
   g.tiles_n = static_cast<int32_t>(cdiv(p.cols, tile));
@@ -184,8 +185,9 @@ int launch_product(const Product& p, int pairs, cudaStream_t st) {
   g.early_w = p.quantized_here;
   CUtensorMap x, w, o;
   std::memset(&o, 0, sizeof(o));
-  if (!encode_map2d(&x, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x.codes, p.red, p.m, p.x.ld, 128, g.box_m,
-                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+  std::memset(&x, 0, sizeof(x));
+  if ((g.x16 == nullptr && !encode_map2d(&x, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x.codes, p.red, p.m, p.x.ld, 128,
+                                         g.box_m, CU_TENSOR_MAP_SWIZZLE_128B)) ||
       !encode_map2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, q.k_in, q.n_out, q.k_in, 128, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B))
     return QLORA_ERR_CUDA;
@@ -194,6 +196,12 @@ int launch_product(const Product& p, int pairs, cudaStream_t st) {
                                  CU_TENSOR_MAP_SWIZZLE_64B))
     return QLORA_ERR_CUDA;
   return launch_fp8_pair(BWD, x, w, o, g, pairs, st);
+}
+
+// Whether a product quantizes its bf16 rows itself: few rows of whole 16-byte
+// pieces, where the split kernel runs.
+bool quantizes(int64_t m, int64_t cols, int64_t red, int dev, int pairs) {
+  return m <= kFp8QuantRows && red % 8 == 0 && !choose(m, cols, cdiv(red, kFp8Block), dev, pairs).pair;
 }
 
 // Workspace of a product over rows of `red` values: the rows' codes and scales.
@@ -226,9 +234,14 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
   if (!aligned(x_bf16, 16) || !aligned(out_bf16, 16) || !aligned(ws, 16)) return QLORA_ERR_ALIGNMENT;
   int sms = 0, pairs = 0;
   if ((s = static_cast<qlora_status_t>(check_current_device(&sms, &pairs))) != QLORA_OK) return s;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_CUDA;
   qlora_fp8_rows_t rows;
+  const bool within = x8 == nullptr && quantizes(m, cols, red, dev, pairs);
   if (x8 != nullptr) {
     rows = *x8;
+  } else if (within) {
+    rows = qlora_fp8_rows_t{m, red, red, nullptr, nullptr, format, 0};
   } else {
     const ProductPlan plan = plan_product(m, red);
     if (ws == nullptr || ws_bytes < plan.total) return QLORA_ERR_WORKSPACE;
@@ -237,8 +250,8 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
                             format, 0};
     if ((s = static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, rows, sms, st))) != QLORA_OK) return s;
   }
-  const Product p{rows, q, out_bf16, m, cols, red, x8 == nullptr};
-  return static_cast<qlora_status_t>(launch_product<BWD>(p, pairs, st));
+  const Product p{rows, within ? x_bf16 : nullptr, q, out_bf16, m, cols, red, x8 == nullptr && !within};
+  return static_cast<qlora_status_t>(launch_product<BWD>(p, dev, pairs, st));
 }
 
 }  // namespace
@@ -284,6 +297,10 @@ qlora_status_t qlora_dequantize_fp8(const qlora_fp8_t* q, void* w_bf16_out, void
 
 size_t qlora_fp8_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in) {
   if (m < 1 || m > kMaxDim || n_out < 1 || n_out > kMaxDim || k_in < 1 || k_in > kMaxDim || k_in % 16 != 0) return 0;
+  int dev = 0, sms = 0, pairs = 0;
+  if (m <= kFp8QuantRows && check_current_device(&sms, &pairs) == QLORA_OK && cudaGetDevice(&dev) == cudaSuccess &&
+      quantizes(m, n_out, k_in, dev, pairs) && quantizes(m, k_in, n_out, dev, pairs))
+    return 0;
   return std::max(plan_product(m, k_in).total, plan_product(m, n_out).total);
 }
 

@@ -24,6 +24,8 @@ struct Fp8Gemm {
   int32_t splits;           // CTAs of a cluster that share a tile's reduction
   int32_t box_m;            // rows of tm_x's boxes
   int32_t early_w;          // the kernel in front has waited for everything before it
+  const __nv_bfloat16* x16; // up to kFp8QuantRows bf16 rows [m x red] (red % 8 == 0), quantized in the kernel; else null
+  int64_t red;
 };
 
 // CTA-pair kernel (fp8_pair.cu). tm_x: rows' codes [m x red], boxes
@@ -36,10 +38,11 @@ cudaError_t set_fp8_pair_attributes();
 
 // Split kernel (fp8_split.cu): 128 x 128 tiles, the reduction over clusters
 // of p.splits (1 to kFp8MaxSplits, at most the number of blocks). tm_x: boxes {128,
-// p.box_m}; tm_w: boxes {128, 128}.
+// p.box_m} (unused with p.x16); tm_w: boxes {128, 128}.
 int launch_fp8_split(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8Gemm& p, cudaStream_t st);
 cudaError_t set_fp8_split_attributes(int dev);
 constexpr int kFp8MaxSplits = 8;
+constexpr int kFp8QuantRows = 4;
 // How many clusters of `splits` CTAs fit on device `dev` at once.
 int fp8_split_clusters(int dev, int splits);
 

@@ -13,6 +13,12 @@
 // share of the rows from all of them, in rank order, and writes bf16. One
 // launch, no atomics, no scratch memory, results that repeat bit for bit.
 //
+// Up to kFp8QuantRows rows in bf16 (QUANT) are quantized here, by the scale warps,
+// straight into the stages, in every CTA anew: one launch less for a single
+// token, and no pass through memory (4096 x 4096 weight, 1 row: 15.1 us of host
+// and 7.5 of device time with a launch of its own; the table of cases has the
+// times now).
+//
 // When the rows were quantized by the kernel launched right before, that
 // kernel has itself waited for everything earlier: the weight's first stages
 // are then requested before waiting for it (p.early_w).
@@ -35,6 +41,7 @@ constexpr int kThreads = 384;
 constexpr int kBufs = 4;
 constexpr int kPartStride = 132;               // fp32 words of a row of partial sums
 constexpr int kScaleChunk = 8, kScaleStride = 132;
+constexpr int kQuantChunk = 4;                 // blocks of a chunk where the rows are quantized here: at once
 constexpr int kRing = 2 * kScaleChunk * kScaleStride * 4;
 constexpr int kSmem = kStages * 32768 + kRing + 1024 + 256;
 static_assert(128 * kPartStride * 4 <= kStages * 32768, "partial sums reuse the stages");
@@ -55,11 +62,12 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
 }
 
 // grid: tiles x splits CTAs, clusters of `splits`; p.box_m rows a row box.
-template <bool W_MN>
+template <bool W_MN, bool QUANT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_fp8_split(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, Fp8Gemm p) {
   constexpr uint32_t HALF = 16384;
   constexpr uint32_t STAGE_BYTES = 2 * HALF;
+  constexpr int CHUNK = QUANT ? kQuantChunk : kScaleChunk;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -69,9 +77,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
   auto bar_empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   auto bar_accf = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
-  auto bar_acce = [&](int b) { return bar0 + 8u * (2 * kStages + kBufs + b); };       // 8 epilogue warps
+  auto bar_acce = [&](int b) { return bar0 + 8u * (2 * kStages + kBufs + b); };       // the live epilogue warps
   auto bar_sf = [&](int c) { return bar0 + 8u * (2 * kStages + 2 * kBufs + c); };      // two scale warps
-  auto bar_se = [&](int c) { return bar0 + 8u * (2 * kStages + 2 * kBufs + 2 + c); };  // 8 epilogue warps
+  auto bar_se = [&](int c) { return bar0 + 8u * (2 * kStages + 2 * kBufs + 2 + c); };  // the live epilogue warps
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(ctl + 8 * (2 * kStages + 2 * kBufs + 4));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const Fp8Abort ab{abort_flag, p.status};
@@ -85,19 +93,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / p.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / p.splits);
   const int rows = min(128, p.m - row0);
+  const int live = (rows + 31) >> 5;           // lane quarters with rows of their own; the others' warps take no part
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar_full(s), 1);
+      mbar_init(bar_full(s), QUANT ? 3 : 1);   // the producer, and the warps that write the rows
       mbar_init(bar_empty(s), 1);
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(bar_accf(b), 1);
-      mbar_init(bar_acce(b), 8);
+      mbar_init(bar_acce(b), 2 * live);
     }
     for (int c = 0; c < 2; ++c) {
       mbar_init(bar_sf(c), 2);
-      mbar_init(bar_se(c), 8);
+      mbar_init(bar_se(c), 2 * live);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -111,13 +120,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   grid_dependency_trigger();
-  bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&tm_x);
+      if (!QUANT) tma_prefetch_desc(&tm_x);
       tma_prefetch_desc(&tm_w);
-      const uint32_t tx = HALF + static_cast<uint32_t>(p.box_m) * 128;
+      const uint32_t tx = HALF + (QUANT ? 0u : static_cast<uint32_t>(p.box_m) * 128);
       auto load_w = [&](int kb, int s) {
         mbar_arrive_expect_tx(bar_full(s), tx);
         const uint32_t dst = base + s * STAGE_BYTES + HALF;
@@ -133,10 +141,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; it < n; ++it) {
         const int s = it % kStages;
         if (it >= first) {
-          if (!(ok = fp8_wait(bar_empty(s), ((it / kStages) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER))) break;
+          if (!fp8_wait(bar_empty(s), ((it / kStages) & 1) ^ 1, ab, QLORA_DEV_TIMEOUT_PRODUCER)) break;
           load_w(kb0 + it, s);
         }
-        tma_load_2d(base + s * STAGE_BYTES, &tm_x, bar_full(s), (kb0 + it) * 128, row0);
+        if (!QUANT) tma_load_2d(base + s * STAGE_BYTES, &tm_x, bar_full(s), (kb0 + it) * 128, row0);
       }
       // every load has landed once its stage's MMAs are done (or, given up on, at full)
       for (int j = max(0, it - kStages); j < it; ++j) drain_wait(bar_full(j % kStages), (j / kStages) & 1);
@@ -177,6 +185,91 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (last >= 0) drain_wait(bar_empty(last), last_ph);
     }
     __syncwarp();
+  } else if (QUANT && warp < 4) {
+    // row 2 (warp - 2) + lane / 16, eight values a lane, the blocks of a chunk at
+    // once: one after the other their latencies made 1.2 us a block
+    static_assert(kFp8QuantRows == 4, "two warps of two rows");
+    grid_dependency_wait();
+    const int l16 = lane & 15, r = 2 * (warp - 2) + (lane >> 4);
+    const bool e5 = p.a_format == kE5M2;
+    const float top = e5 ? fp8_top<kE5M2>() : fp8_top<kE4M3>();
+    const int ob = col0 >> 7;
+    uint4 v[CHUNK];
+    float w = 0.0f;                            // lane i < CHUNK of warp 2: the weight's scale of block i
+    auto request = [&](int k0) {
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) {
+        const int64_t col = static_cast<int64_t>(k0 + i) * 128 + 8 * l16;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows && k0 + i < kb1 && col < p.red)      // p.red % 8 == 0
+          v[i] = __ldg(reinterpret_cast<const uint4*>(p.x16 + r * p.red + col));
+      }
+      if (warp == 2 && lane < CHUNK && k0 + lane < kb1) w = __ldg(p.sw + ob * p.sw_out + (k0 + lane) * p.sw_red);
+    };
+    int c = 0, s = 0;
+    uint32_t cph = 1, ph = 1;
+    request(kb0);
+    for (int k0 = kb0; k0 < kb1; k0 += CHUNK) {
+      const int n = min(CHUNK, kb1 - k0);
+      float a[CHUNK];
+      uint32_t lo[CHUNK], hi[CHUNK];
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) {
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        a[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[i] = fmaxf(a[i], fmaxf(fp8_mag(__uint_as_float(u[j] << 16)), fp8_mag(__uint_as_float(u[j] & 0xFFFF0000u))));
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < CHUNK; ++i) a[i] = fmaxf(a[i], __shfl_xor_sync(0xFFFFFFFFu, a[i], o));
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) {
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        a[i] = fmaxf(a[i], kFp8Least);
+        const float inv = top / a[i];
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = fp8_scaled(__uint_as_float(u[j] << 16), inv);
+          f[2 * j + 1] = fp8_scaled(__uint_as_float(u[j] & 0xFFFF0000u), inv);
+        }
+        lo[i] = e5 ? fp8_pack4<kE5M2>(f[0], f[1], f[2], f[3]) : fp8_pack4<kE4M3>(f[0], f[1], f[2], f[3]);
+        hi[i] = e5 ? fp8_pack4<kE5M2>(f[4], f[5], f[6], f[7]) : fp8_pack4<kE4M3>(f[4], f[5], f[6], f[7]);
+      }
+      if (!fp8_token(bar_se(c), cph)) fp8_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER);
+      __syncwarp();
+      const uint32_t slot = ring + c * (CHUNK * kScaleStride * 4);
+      if (warp == 2 && lane < CHUNK) sts32(slot + lane * (kScaleStride * 4) + 4 * 128, __float_as_uint(w));
+      request(k0 + CHUNK);
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i) {
+        if (i >= n) break;
+        if (!fp8_token(bar_empty(s), ph)) fp8_wait(bar_empty(s), ph, ab, QLORA_DEV_TIMEOUT_PRODUCER);
+        __syncwarp();
+        if (r < rows) {
+          // the 128-byte swizzle that a tensor copy would have made
+          const uint32_t at = base + s * STAGE_BYTES + r * 128 + (((l16 >> 1) ^ (r & 7)) << 4) + 8 * (l16 & 1);
+          sts32(at, lo[i]);
+          sts32(at + 4, hi[i]);
+          if (l16 == 0) sts32(slot + i * (kScaleStride * 4) + 4 * r, __float_as_uint(a[i] / top));
+        }
+        fence_proxy_async_smem();              // the tensor core reads what was written here
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_full(s));
+          if (i + 1 == n) mbar_arrive(bar_sf(c));
+        }
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      c ^= 1;
+      if (c == 0) cph ^= 1;
+    }
   } else if (warp < 4) {
     // scales: as in the pair kernel, a chunk requested while the one before is at work
     grid_dependency_wait();
@@ -209,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c == 0) cph ^= 1;
       request(k0 + kScaleChunk);
     }
-  } else {
+  } else if ((warp & 3) < live) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 64 * half;
     const uint32_t ring_x = ring + 4 * (32 * quarter + lane), ring_w = ring + 4 * 128;
@@ -224,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (left == 0) {
         if (!fp8_token(bar_sf(c), cph)) fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
         __syncwarp();
-        left = min(kb, kScaleChunk);
-        slot = c * (kScaleChunk * kScaleStride * 4);
+        left = min(kb, CHUNK);
+        slot = c * (CHUNK * kScaleStride * 4);
       }
       const float s = __uint_as_float(lds32(ring_x + slot)) * __uint_as_float(lds32(ring_w + slot));
       const uint64_t s2 = f2(s, s);
@@ -324,16 +417,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool W_MN>
+template <bool W_MN, bool QUANT>
 int launch(const CUtensorMap& x, const CUtensorMap& w, const Fp8Gemm& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(p.tiles_m) * static_cast<unsigned>(p.tiles_n) * p.splits;
-  return host::launch_pdl(k_fp8_split<W_MN>, dim3(grid), dim3(kThreads), kSmem, st, p.splits, x, w, p);
+  return host::launch_pdl(k_fp8_split<W_MN, QUANT>, dim3(grid), dim3(kThreads), kSmem, st, p.splits, x, w, p);
 }
 
 }  // namespace
 
 int launch_fp8_split(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8Gemm& p, cudaStream_t st) {
-  return w_mn ? launch<true>(tm_x, tm_w, p, st) : launch<false>(tm_x, tm_w, p, st);
+  if (p.x16 != nullptr) return w_mn ? launch<true, true>(tm_x, tm_w, p, st) : launch<false, true>(tm_x, tm_w, p, st);
+  return w_mn ? launch<true, false>(tm_x, tm_w, p, st) : launch<false, false>(tm_x, tm_w, p, st);
 }
 
 namespace {
@@ -341,9 +435,11 @@ int g_clusters[64][kFp8MaxSplits + 1];   // written by the device check, under i
 }
 
 cudaError_t set_fp8_split_attributes(int dev) {
-  cudaError_t e = cudaFuncSetAttribute(k_fp8_split<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_fp8_split<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(k_fp8_split<false, false>, a, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_fp8_split<true, false>, a, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_fp8_split<false, true>, a, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_fp8_split<true, true>, a, kSmem);
   for (int s = 1; e == cudaSuccess && s <= kFp8MaxSplits; ++s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -356,7 +452,7 @@ cudaError_t set_fp8_split_attributes(int dev) {
     cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&g_clusters[dev][s], k_fp8_split<false>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&g_clusters[dev][s], k_fp8_split<false, false>, &cfg);
   }
   return e;
 }

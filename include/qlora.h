@@ -347,10 +347,10 @@ QLORA_API qlora_status_t qlora_dequantize_fp8(const qlora_fp8_t *q, void *w_bf16
 /* Quantize bf16 rows x [rows x cols] (dense) into out. rows == 0 is a no-op. */
 QLORA_API qlora_status_t qlora_quantize_fp8_rows(const void *x_bf16, const qlora_fp8_rows_t *out, void *stream);
 
-/* Workspace bytes for qlora_fp8_linear_fwd and _bwd at these sizes (the rows
- * in 8 bits where they come in bf16, and fp32 partial sums where the
- * reduction is split over SMs); 0 for sizes out of range. Depends on the
- * current device's SM count. */
+/* Workspace bytes for qlora_fp8_linear_fwd and _bwd at these sizes: the rows
+ * in 8 bits, where they come in bf16. 0 where both calls need none (up to 4
+ * rows whose lengths are multiples of 8 are quantized within the product) and
+ * for sizes out of range. Depends on the current device's SM count. */
 QLORA_API size_t qlora_fp8_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in);
 
 /* y [m x N] bf16 = x W^T. x comes either as bf16 [m x K] (quantized to e4m3

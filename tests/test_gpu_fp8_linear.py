@@ -93,7 +93,7 @@ def test_quantize_weight_bit_exact(q, n, k):
     assert torch.equal(torch.nan_to_num(back, 7.0), torch.nan_to_num(want, 7.0))
 
 
-SHAPES = [(1, 64, 64), (1, 1, 16), (2, 4096, 4096), (8, 1003, 1040), (9, 257, 272), (16, 384, 4096), (17, 130, 4112),
+SHAPES = [(1, 64, 64), (3, 1003, 1040), (4, 520, 4112), (4, 1000, 272), (5, 264, 1040), (1, 1, 16), (2, 4096, 4096), (8, 1003, 1040), (9, 257, 272), (16, 384, 4096), (17, 130, 4112),
           (33, 1000, 512), (64, 11008, 1024), (127, 129, 144), (128, 256, 128), (129, 512, 640), (200, 4096, 1024),
           (256, 256, 256), (257, 1003, 1040), (300, 264, 2064), (513, 777, 1296), (1000, 2048, 512), (1300, 2307, 272), (1300, 2306, 272), (2100, 1500, 1296), (600, 5000, 1040)]
 
