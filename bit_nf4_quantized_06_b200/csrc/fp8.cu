@@ -126,10 +126,10 @@ struct Product {
 // The tile shape and the split, by an estimate of the time in microseconds.
 // Measured on B200 with rows already in 8 bits:
 //   pair kernel   5 + waves (1.5 + 0.40 blocks): 512 rows x 4096 x 4096 17.8, 1024 rows 18.9, 2048 rows 33.6
-//   split kernel  waves (4.6 + S (0.1 + 0.002 rows) + 0.28 ceil(blocks / S)), a wave being the
-//                 clusters of S CTAs that are resident at once:
-//                 4096 x 4096 weight, 1 row: 11.8 (S = 1), 7.8 (2), 6.3 (4), 13.9 (8, two waves);
-//                 128 rows: 13.8, 10.1, 8.7, 21.9; 512 rows, S = 1: 14.8; 1024 rows: 29.0
+//   split kernel  waves (4.7 + 0.004 S rows + (0.2 + 0.0006 rows) ceil(blocks / S)), a wave being
+//                 the clusters of S CTAs that are resident at once:
+//                 4096 x 4096 weight, 1 row: 10.6 (S = 1), 7.2 (2), 6.0 (4), 13.5 (8, two waves);
+//                 128 rows: 12.9, 9.7, 8.4, 21.9; 512 rows, S = 1: 13.5; 1024 rows: 26.9
 struct Choice {
   bool pair;
   int splits;
@@ -146,8 +146,8 @@ Choice choose(int64_t m, int64_t cols, int64_t kblocks, int dev, int pairs) {
     const int resident = fp8_split_clusters(dev, s);
     if (resident < 1) continue;
     const double waves = static_cast<double>(cdiv(tiles, resident));
-    const double cost =
-        waves * (4.6 + (s > 1 ? s * (0.1 + 0.002 * rows) : 0.0) + 0.28 * static_cast<double>(cdiv(kblocks, s)));
+    const double cost = waves * (4.7 + (s > 1 ? 0.004 * s * rows : 0.0) +
+                                 (0.2 + 0.0006 * rows) * static_cast<double>(cdiv(kblocks, s)));
     if (cost < best_cost) {
       best_cost = cost;
       best = Choice{false, s};

@@ -312,16 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b = 0, c = 0, left = 0;
     uint32_t bph = 0, cph = 0, slot = 0;
     bool ready = false;              // token of bar_accf(b)
-#pragma unroll 1
-    for (int kb = kb1 - kb0; kb > 0; --kb) {
+    // the factor of the next block, `more` of them to come
+    auto next_scale = [&](int more) -> float {
       if (left == 0) {
         if (!fp8_token(bar_sf(c), cph)) fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
         __syncwarp();
-        left = min(kb, CHUNK);
+        left = min(more, CHUNK);
         slot = c * (CHUNK * kScaleStride * 4);
       }
       const float s = __uint_as_float(lds32(ring_x + slot)) * __uint_as_float(lds32(ring_w + slot));
-      const uint64_t s2 = f2(s, s);
       slot += kScaleStride * 4;
       if (--left == 0) {
         __syncwarp();
@@ -329,23 +328,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         c ^= 1;
         if (c == 0) cph ^= 1;
       }
+      return s;
+    };
+    float s = next_scale(kb1 - kb0);
+#pragma unroll 1
+    for (int kb = kb1 - kb0; kb > 0; --kb) {
+      const uint64_t s2 = f2(s, s);
       if (!ready) fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
       __syncwarp();
       tc_fence_after();
-      const uint32_t t = tbase + b * 128;
+      const uint32_t t = tbase + b * 128, acce = bar_acce(b);
+      if (++b == kBufs) {
+        b = 0;
+        bph ^= 1;
+      }
       uint32_t ra[16], rb[16], rc[16], rd[16];
       tmem_ld_32x32b_x16(t, ra);
       tmem_ld_32x32b_x16(t + 16, rb);
       tmem_ld_32x32b_x16(t + 32, rc);
       tmem_ld_32x32b_x16(t + 48, rd);
+      if (kb > 1) s = next_scale(kb - 1);      // while the sums are on their way
       tc_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_acce(b));
-      if (++b == kBufs) {
-        b = 0;
-        bph ^= 1;
-      }
+      if (lane == 0) mbar_arrive(acce);
       ready = fp8_token(bar_accf(b), bph);
       promote16(acc, ra, s2);
       promote16(acc + 8, rb, s2);
