@@ -3,7 +3,11 @@
     python -m bit_nf4_quantized_06_b200.profile_case --op fwd --workload 7b-mlp --iters 3 [--schedule auto|dp|sk]
 
 Ops: quantize, dequantize, fwd (tensor-core path), bwd, gemv (decode path),
-merge (LoRA merge for export), adamw (adapter optimizer step, states on device).
+merge (LoRA merge for export), adamw (adapter optimizer step, states on device);
+fp8-quantize, fp8-fwd, fp8-bwd (the merged weight in 8 bits, x and dY quantized
+within the call), norm-fp8-fwd (RMS norm with the residual's addition into 8-bit
+rows, then the 8-bit product), norm-bwd, adamw-multi (every adapter of 32 layers
+of such a projection in one call, states in 8 bits).
 Workloads: tiny, decode, 7b-mlp, 65b-gate, 65b-down, decode-65b-gate. The inputs are the
 seeded synthetic tensors of ``synth``; every call goes through the C ABI.
 Prints one line with the mean device time per call (CUDA events); numbers
@@ -32,7 +36,9 @@ WORKLOADS = {"tiny": synth.TINY, "decode": synth.DECODE, "7b-mlp": synth.MLP7B,
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", choices=["quantize", "dequantize", "fwd", "bwd", "gemv", "merge", "adamw"], required=True)
+    ap.add_argument("--op", choices=["quantize", "dequantize", "fwd", "bwd", "gemv", "merge", "adamw", "fp8-quantize",
+                                       "fp8-fwd", "fp8-bwd", "norm-fp8-fwd", "norm-bwd", "adamw-multi"],
+                    required=True)
     ap.add_argument("--workload", choices=sorted(WORKLOADS), default="7b-mlp")
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--schedule", choices=["auto", "dp", "sk"], default="auto",
@@ -53,6 +59,15 @@ def main(argv=None):
     master = torch.zeros(na, device="cuda")
     grad = torch.full((na,), 1e-3, device="cuda")
     m_st, v_st = torch.zeros(na, device="cuda"), torch.zeros(na, device="cuda")
+    if a.op.startswith(("fp8", "norm")):
+        w8 = q.qlora_quantize_fp8(q.qlora_merge_lora(qw, aa, bb, p.alpha))
+        gamma = torch.ones(p.k, dtype=torch.bfloat16, device="cuda")
+        _, h, rstd = q.qlora_rmsnorm_fwd(x, gamma, residual=x)
+        dx = torch.empty_like(x)
+    if a.op == "adamw-multi":
+        adapters = [v.float() for v in (aa, bb) for _ in range(32)]
+        group = q.AdamWGroup(adapters, params=[v.bfloat16() for v in adapters], bits=8)
+        grads = [torch.full_like(v, 1e-3) for v in adapters]
 
     def call():
         if a.op == "quantize":
@@ -65,6 +80,18 @@ def main(argv=None):
             q.qlora_merge_lora(qw, aa, bb, p.alpha, out=w_out)
         elif a.op == "adamw":
             q.qlora_adamw_step(master, grad, m_st, v_st, 1)
+        elif a.op == "fp8-quantize":
+            q.qlora_quantize_fp8(w_out, out=w8)
+        elif a.op == "fp8-fwd":
+            q.qlora_fp8_linear_fwd(w8, x, y=y)
+        elif a.op == "fp8-bwd":
+            q.qlora_fp8_linear_bwd(w8, dy, dx=dx)
+        elif a.op == "norm-fp8-fwd":
+            q.qlora_fp8_linear_fwd(w8, q.qlora_rmsnorm_fwd(x, gamma, residual=x, fp8=True)[0], y=y)
+        elif a.op == "norm-bwd":
+            q.qlora_rmsnorm_bwd(x, h, gamma, rstd, dres=x)
+        elif a.op == "adamw-multi":
+            q.qlora_adamw_multi(group, grads, 1)
         elif a.op == "gemv":
             q.qlora_linear_fwd_ex(qw, x, aa, bb, p.alpha, path=q.FWD_GEMV, y=y, ws=ws, want_u=False)
         else:

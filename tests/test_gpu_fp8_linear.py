@@ -139,12 +139,11 @@ def test_forward_in_e5m2_rows(q):
         _check_product(y, fp8.rows_values(xc, xs, fp8.E5M2), fp8.weight_values(codes, scales))
 
 
-@pytest.mark.parametrize("m", [1, 9, 40, 300])
-def test_scales_of_every_block_count(q, m):
+@pytest.mark.parametrize("m,n,k", [(1, 300, 656), (9, 300, 656), (40, 300, 656), (300, 300, 656), (1300, 2307, 1296)])
+def test_scales_of_every_block_count(q, m, n, k):
     # each block with a scale of its own size: a scale taken from a neighbour shows
     rng = np.random.default_rng(m)
-    n, k = 300, 656
-    size = np.exp2(rng.integers(-9, 10, (3, 6))).astype(np.float32)
+    size = np.exp2(rng.integers(-9, 10, (-(-n // 128), -(-k // 128)))).astype(np.float32)
     w = rng.standard_normal((n, k)).astype(np.float32) * np.repeat(np.repeat(size, 128, 0), 128, 1)[:n, :k]
     codes, scales = fp8.quantize_weight(w)
     qw = q.FP8Weight(torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn), torch.from_numpy(scales).cuda())
@@ -160,10 +159,10 @@ def test_scales_of_every_block_count(q, m):
             _check_product(q.qlora_fp8_linear_bwd(qw, x.cuda()), values, wv.T)
 
 
-@pytest.mark.parametrize("m", [1, 12, 70, 260])
-def test_values_that_are_not_finite_stay_in_their_rows(q, m):
+@pytest.mark.parametrize("m,n", [(1, 200), (12, 200), (70, 200), (260, 200), (1300, 2307)])
+def test_values_that_are_not_finite_stay_in_their_rows(q, m, n):
     rng = np.random.default_rng(m + 1)
-    w = q.qlora_quantize_fp8(_bf16(rng, 200, 272).cuda())
+    w = q.qlora_quantize_fp8(_bf16(rng, n, 272).cuda())
     x = _bf16(rng, m, 272).cuda()
     y0 = q.qlora_fp8_linear_fwd(w, x)
     x[m // 2, 5] = float("inf")
@@ -171,6 +170,46 @@ def test_values_that_are_not_finite_stay_in_their_rows(q, m):
     assert torch.all(torch.isnan(y[m // 2]))
     keep = torch.arange(m, device="cuda") != m // 2
     assert torch.equal(y[keep], y0[keep])
+
+
+def test_rows_of_a_wider_buffer(q):
+    # rows further apart than their length, in memory whose other bytes are not codes of theirs
+    rng = np.random.default_rng(12)
+    w = q.qlora_quantize_fp8(_bf16(rng, 300, 400).cuda())
+    for m in (1, 6, 150, 1300):
+        x = _bf16(rng, m, 400).cuda()
+        rows = q.qlora_quantize_fp8_rows(x)
+        wide = torch.full((m, 512), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[:, 16:416] = rows.codes.view(torch.uint8)
+        shifted = q.FP8Rows(wide.view(torch.float8_e4m3fn)[:, 16:416], rows.scales)
+        assert torch.equal(q.qlora_fp8_linear_fwd(w, shifted), q.qlora_fp8_linear_fwd(w, rows))
+
+
+def test_many_calls_in_flight(q):
+    # products, norms and quantizers launched one behind the other, each started before the one in front is
+    # done: every result as when called alone
+    rng = np.random.default_rng(13)
+    w = [q.qlora_quantize_fp8(_bf16(rng, 512, 512, scale=0.05).cuda()) for _ in range(3)]
+    gamma = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    for m in (1, 33, 300, 1500):
+        x = _bf16(rng, m, 512).cuda()
+
+        def chain(wait):
+            y, out = x, []
+            for i in range(9):
+                y8, h, _ = q.qlora_rmsnorm_fwd(y, gamma, residual=x, fp8=True)
+                y = q.qlora_fp8_linear_fwd(w[i % 3], y8)
+                d = q.qlora_fp8_linear_bwd(w[i % 3], y)
+                if wait:
+                    torch.cuda.synchronize()
+                out += [y, h, d]
+            return out
+
+        want = chain(True)
+        for _ in range(3):
+            got = chain(False)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert q.qlora_device_status() == (0, 0)
 
 
 def test_gradient_is_the_transpose(q):

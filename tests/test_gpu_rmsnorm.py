@@ -17,7 +17,7 @@ from oracle import fp8, norm
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
-WIDTHS = [(1, 1), (3, 7), (2, 64), (5, 128), (9, 129), (700, 256), (33, 264), (4, 1000), (257, 1024), (3, 4096), (150, 4099),
+WIDTHS = [(1, 1), (3, 7), (70, 8), (2, 64), (1300, 4104), (1300, 2501), (5, 128), (9, 129), (700, 256), (33, 264), (4, 1000), (257, 1024), (3, 4096), (150, 4099),
           (2, 8192), (2, 12344), (3, 16385), (2, 20000), (2, 33000), (3, 40001)]
 
 
