@@ -463,11 +463,11 @@ def _elsewhere(dev, stream, where):
         if stream.device.index != dev:
             raise ValueError(f"{where}: the stream belongs to another device than the tensors")
         return torch.cuda.stream(stream)
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _raw_stream(dev):
-    return _torch()._C._cuda_getCurrentRawStream(dev)
+    return _torch_module._C._cuda_getCurrentRawStream(dev)
 
 
 def _is(t, dtype, shape, dev):
@@ -476,7 +476,7 @@ def _is(t, dtype, shape, dev):
 
 def _matrix(rows, cols, dtype, device):
     # the cheapest of torch's allocating calls for a shape of two
-    return _torch().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+    return _torch_module.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _want(ok, where, what):
@@ -538,12 +538,12 @@ class FP8Rows:
     @classmethod
     def empty(cls, rows, cols, fmt=FP8_E4M3, device="cuda"):
         torch = _torch()
-        dtype, ld = _fp8_dtype(fmt), -(-cols // 16) * 16
+        dtype, ld = _fp8_dtype(fmt), (cols + 15) & ~15
         codes = _matrix(rows, ld, dtype, device)
         self = cls.__new__(cls)      # right by construction: no checks
         self.codes = codes if ld == cols else codes[:, :cols]
-        self.scales = _matrix(rows, -(-cols // 128), torch.float32, device)
-        self.ld, self.fmt = ld, int(fmt)
+        self.scales = _matrix(rows, (cols + 127) >> 7, torch.float32, device)
+        self.ld, self.fmt = ld, fmt
         return self
 
     def struct(self):
@@ -607,26 +607,32 @@ def qlora_fp8_workspace_bytes(m, n_out, k_in):
 
 
 def _fp8_product(call, where, q, x, fmt, cols_in, cols_out, out, ws):
-    torch = _torch()
+    torch = _torch_module
     dev = q.codes.get_device()
-    rows = x.struct() if isinstance(x, FP8Rows) else None
-    src = x.codes if rows is not None else x
-    _want(src.dim() == 2 and src.shape[1] == cols_in and src.get_device() == dev and
-          (rows is not None or (src.dtype is torch.bfloat16 and src.is_contiguous())), where,
-          f"rows must be FP8Rows or contiguous bf16 [m, {cols_in}] on the weight's device")
+    rows = x.struct() if type(x) is FP8Rows else None
+    src = x if rows is None else x.codes
+    if not (src.dim() == 2 and src.shape[1] == cols_in and src.get_device() == dev and
+            (rows is not None or (src.dtype is torch.bfloat16 and src.is_contiguous()))):
+        raise ValueError(f"{where}: rows must be FP8Rows or contiguous bf16 [m, {cols_in}] on the weight's device")
     m = src.shape[0]
     if out is None:
         out = _matrix(m, cols_out, torch.bfloat16, src.device)
-    else:
-        _want(_is(out, torch.bfloat16, (m, cols_out), dev), where, f"the output must be contiguous bf16 [m, {cols_out}]")
+    elif not _is(out, torch.bfloat16, (m, cols_out), dev):
+        raise ValueError(f"{where}: the output must be contiguous bf16 [m, {cols_out}]")
+    at = size = 0
     if ws is not None:
         _want(ws.get_device() == dev and ws.is_contiguous(), where, "the workspace must be contiguous, on the weight's device")
+        at, size = ws.data_ptr(), ws.numel() * ws.element_size()
     elif rows is None:           # rows already in 8 bits need none, nor do a few
-        need = lib.qlora_fp8_workspace_bytes(m, q.n_out, q.k_in)
-        ws = torch.empty(need, dtype=torch.uint8, device=src.device) if need else None
-    at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-    args = (q.struct(), None if rows is not None else x.data_ptr(), rows) + (() if fmt is None else (int(fmt),))
-    _check(call(*args, m, out.data_ptr(), at, size, _raw_stream(dev)), where)
+        size = lib.qlora_fp8_workspace_bytes(m, q.n_out, q.k_in)
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=src.device)
+            at = ws.data_ptr()
+    x16, stream = x.data_ptr() if rows is None else None, _raw_stream(dev)
+    st = (call(q.struct(), x16, rows, m, out.data_ptr(), at, size, stream) if fmt is None else
+          call(q.struct(), x16, rows, int(fmt), m, out.data_ptr(), at, size, stream))
+    if st:
+        raise QloraError(st, where)
     return out
 
 
@@ -658,33 +664,36 @@ def qlora_rmsnorm_fwd(x, gamma, eps=1e-6, residual=None, fp8=False, fmt=FP8_E4M3
     if (at := _elsewhere(dev, stream, "qlora_rmsnorm_fwd")) is not None:
         with at:
             return qlora_rmsnorm_fwd(x, gamma, eps, residual, fp8, fmt, y, h, rstd)
-    _want(x.dim() == 2, "qlora_rmsnorm_fwd", "x must be a matrix")
-    rows, d = x.shape
-    bf16 = torch.bfloat16
-    _want(_is(x, bf16, x.shape, dev) and _is(gamma, bf16, (d,), dev) and
-          (residual is None or _is(residual, bf16, x.shape, dev)), "qlora_rmsnorm_fwd",
-          "x, residual [rows, d] and gamma [d] must be contiguous bf16 on one device")
+    bf16, shape, device = torch.bfloat16, x.shape, x.device
+    if not (len(shape) == 2 and x.dtype is bf16 and x.is_contiguous() and _is(gamma, bf16, shape[1:], dev) and
+            (residual is None or _is(residual, bf16, shape, dev))):
+        raise ValueError("qlora_rmsnorm_fwd: x, residual [rows, d] and gamma [d] must be contiguous bf16 on one device")
+    rows, d = shape
     if y is None:
-        y = FP8Rows.empty(rows, d, fmt, x.device) if fp8 else torch.empty_like(x)
+        y = FP8Rows.empty(rows, d, fmt, device) if fp8 else torch.empty_like(x)
     else:
-        _want((isinstance(y, FP8Rows) and y.codes.shape == x.shape and y.codes.get_device() == dev) if fp8
-              else _is(y, bf16, x.shape, dev), "qlora_rmsnorm_fwd", "y has another type, shape or device")
+        _want((isinstance(y, FP8Rows) and y.codes.shape == shape and y.codes.get_device() == dev) if fp8
+              else _is(y, bf16, shape, dev), "qlora_rmsnorm_fwd", "y has another type, shape or device")
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
     else:
         _want(_is(rstd, torch.float32, (rows,), dev), "qlora_rmsnorm_fwd", "rstd must be fp32 [rows]")
-    if residual is None:
-        _want(h is None, "qlora_rmsnorm_fwd", "h is written only with a residual")
-    elif h is None:
-        h = torch.empty_like(x)
+    at_res = at_h = None
+    if residual is not None:
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            _want(_is(h, bf16, shape, dev), "qlora_rmsnorm_fwd", "h must be contiguous bf16 [rows, d]")
+        at_res, at_h = residual.data_ptr(), h.data_ptr()
     else:
-        _want(_is(h, bf16, x.shape, dev), "qlora_rmsnorm_fwd", "h must be contiguous bf16 [rows, d]")
-    y8 = y.struct() if fp8 else None
-    st = lib.qlora_rmsnorm_fwd(x.data_ptr(), None if residual is None else residual.data_ptr(), gamma.data_ptr(), rows, d,
-                               eps, None if h is None else h.data_ptr(), None if fp8 else y.data_ptr(), y8,
-                               rstd.data_ptr(), _raw_stream(dev))
-    _check(st, "qlora_rmsnorm_fwd")
-    return y, (x if residual is None else h), rstd
+        _want(h is None, "qlora_rmsnorm_fwd", "h is written only with a residual")
+        h = x
+    y16, y8 = (None, y.struct()) if fp8 else (y.data_ptr(), None)
+    st = lib.qlora_rmsnorm_fwd(x.data_ptr(), at_res, gamma.data_ptr(), rows, d, eps, at_h, y16, y8, rstd.data_ptr(),
+                               _raw_stream(dev))
+    if st:
+        raise QloraError(st, "qlora_rmsnorm_fwd")
+    return y, h, rstd
 
 
 def qlora_rmsnorm_workspace_bytes(rows, d):
@@ -792,6 +801,7 @@ def qlora_adamw_multi(group, grads, step, lr=1e-4, betas=(0.9, 0.999), eps=1e-8,
     if (at := _elsewhere(dev, stream, "qlora_adamw_multi")) is not None:
         with at:
             return qlora_adamw_multi(group, grads, step, lr, betas, eps, weight_decay)
+    # a few C-level passes over the lists: with hundreds of tensors this is most of the call's host time
     _want(list(map(T.numel, grads)) == group.sizes, "qlora_adamw_multi", "grads must match the masters in number and length")
     _want(set(map(_dtype_of, grads)) == {torch.float32} and all(map(T.is_contiguous, grads)) and
           set(map(T.get_device, grads)) == {dev}, "qlora_adamw_multi", "grads must be contiguous fp32 on the group's device")
