@@ -15,13 +15,23 @@
 //
 // Up to kFp8QuantRows rows in bf16 (QUANT) are quantized here, by the scale warps,
 // straight into the stages, in every CTA anew: one launch less for a single
-// token, and no pass through memory (4096 x 4096 weight, 1 row: 15.1 us of host
-// and 7.5 of device time with a launch of its own; the table of cases has the
-// times now).
+// token, and no pass through memory (4096 x 4096 weight, 1 row: 10.1 us a call
+// from Python and 7.2 on the device; with a launch of its own 15.1 and 7.5. More
+// rows than a pass of the two warps holds made the device time longer: 16 rows
+// 14.3 us).
 //
 // When the rows were quantized by the kernel launched right before, that
 // kernel has itself waited for everything earlier: the weight's first stages
 // are then requested before waiting for it (p.early_w).
+//
+// Measured (rows in 8 bits, device time): 4096 x 4096 weight, 1 row, S = 4: 6.0 us
+// (2.8 TB/s of weight); 11008 x 4096, 37 rows, S = 1: 12.9 us (3.5 TB/s). Of that
+// some 5 us pass before and after the stream (launch, barriers and tensor
+// memory, the first load, joining and writing), and a reduction block costs a
+// CTA some 450 cycles of epilogue, where the tensor core needs 256. Two groups of
+// epilogue warps on alternate blocks made a block shorter (8 rows, 86 blocks in
+// one CTA: 23.6 -> 24.9 with the longer end: no gain) and were not kept, nor were
+// up to eleven narrower stages for few rows (the same time).
 //
 // Warps (384 threads): 0 TMA; 1 tensor-memory allocation and MMA issue; 2-3
 // scales; 4-11 epilogue (lane quarter = warp % 4, output half = (warp - 4) / 4).

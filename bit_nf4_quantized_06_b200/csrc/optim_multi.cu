@@ -17,9 +17,10 @@
 // bits). A CTA takes chunks of eight blocks, a block a warp, through a ring of
 // stages in shared memory: one stage holds a chunk's master values, gradients
 // and states, filled by four bulk copies that are requested several chunks
-// ahead. (8 bits, 160 million values: loads to registers kept 61 KB in flight
-// on an SM, 573 us; a ring a warp, of 256-byte copies, was bound by the copies'
-// number, 816 us.)
+// ahead. Measured, 8 bits, 160 million values in 448 tensors: 457 us, 6.3 TB/s
+// (loads to registers kept 61 KB in flight on an SM, 573 us; a ring a warp, of
+// 256-byte copies, was bound by the copies' number, 816 us); 32 bits, 134
+// million values: 688 us, 5.9 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <vector>
