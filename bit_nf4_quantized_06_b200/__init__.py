@@ -777,6 +777,7 @@ class AdamWGroup:
             _want(_is(t, ty, (n,), dev), "AdamWGroup", f"{name} must be contiguous {ty} of {n} values on the masters' device")
             setattr(self, name, t)
         self._at = [t.data_ptr() for t in self.masters], [t.data_ptr() for t in self.params or []]
+        self._states_at = self._states()
         desc = np.zeros((len(self.sizes), 8), dtype=np.uint64)     # rows of qlora_adamw_tensor_t
         desc[:, 0] = self._at[0]
         if self.params is not None:
@@ -790,6 +791,10 @@ class AdamWGroup:
             desc[:, 6] = self.v_scales.data_ptr() + blocks
         desc[:, 7] = self.sizes
         self._desc = desc
+
+    def _states(self):
+        # scales None: 32-bit states
+        return [None if t is None else t.data_ptr() for t in (self.m, self.v, self.m_scales, self.v_scales)]
 
 
 def qlora_adamw_multi(group, grads, step, lr=1e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, stream=None):
@@ -806,8 +811,8 @@ def qlora_adamw_multi(group, grads, step, lr=1e-4, betas=(0.9, 0.999), eps=1e-8,
     _want(set(map(_dtype_of, grads)) == {torch.float32} and all(map(T.is_contiguous, grads)) and
           set(map(T.get_device, grads)) == {dev}, "qlora_adamw_multi", "grads must be contiguous fp32 on the group's device")
     _want(list(map(T.data_ptr, group.masters)) == group._at[0] and
-          list(map(T.data_ptr, group.params or ())) == group._at[1], "qlora_adamw_multi",
-          "a master's or param's storage has moved since the group was made")
+          list(map(T.data_ptr, group.params or ())) == group._at[1] and group._states() == group._states_at,
+          "qlora_adamw_multi", "a master's, param's or state's storage has moved since the group was made")
     desc = group._desc.copy()
     desc[:, 2] = list(map(T.data_ptr, grads))
     hp = AdamwParams(lr, betas[0], betas[1], eps, weight_decay, step)

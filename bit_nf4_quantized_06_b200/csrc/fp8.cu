@@ -222,7 +222,7 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
                        void* out_bf16, void* ws, size_t ws_bytes, cudaStream_t st) {
   qlora_status_t s = check_weight(q);
   if (s != QLORA_OK) return s;
-  if (format != QLORA_FP8_E4M3 && format != QLORA_FP8_E5M2) return QLORA_ERR_INVALID_ARG;
+  if (x8 == nullptr && format != QLORA_FP8_E4M3 && format != QLORA_FP8_E5M2) return QLORA_ERR_INVALID_ARG;
   if (m < 0 || m > kMaxDim) return QLORA_ERR_SHAPE;
   const int64_t red = BWD ? q->n_out : q->k_in, cols = BWD ? q->k_in : q->n_out;
   if (x8 != nullptr) {

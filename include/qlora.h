@@ -315,7 +315,10 @@ QLORA_API qlora_status_t qlora_adamw_staged(float *master, void *param_bf16, con
  *   weight: 128 x 128 blocks, e4m3; the last blocks of either axis are short
  *   rows:   blocks of 128 consecutive columns of one row, e4m3 or e5m2
  * Products of codes are summed in fp32 within a block of 128 of the
- * reduction, multiplied by the two scales, and summed over blocks in fp32. */
+ * reduction, multiplied by the two scales, and summed over blocks in fp32, in
+ * a fixed order: results repeat bit for bit. The output overlaps no other
+ * buffer. Calls that can overlap on the GPU (on two streams, in two graphs)
+ * need workspaces of their own, here and for qlora_rmsnorm_bwd. */
 typedef enum { QLORA_FP8_E4M3 = 0, QLORA_FP8_E5M2 = 1 } qlora_fp8_format_t;
 
 /* Weight in e4m3, row-major, caller-owned device buffers. */
@@ -407,8 +410,10 @@ QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void *dy_bf16, const void *h_bf
  *     needs. A gradient that is not finite spoils its own value only, as with
  *     32-bit states. The step itself uses the new m and v before they are
  *     rounded to 8 bits.
- * `tensors` is a host array; it is read during the call and may be reused at
- * once. Buffers of different tensors must not overlap: the same master, m or
+ * `tensors` is a host array; it is read during the call (a captured call
+ * keeps the pointers and the step number that it was captured with) and may
+ * be reused at once. All buffers are device memory (states in pinned host
+ * memory stay with qlora_adamw_step and _staged). Buffers of different tensors must not overlap: the same master, m or
  * v twice is refused. n == 0 entries are skipped. fp32 pointers 4-byte,
  * param_bf16 (may be NULL) 2-byte aligned; tensors with 16-byte aligned
  * buffers (8-byte for bf16 and codes) take the wide loads. */

@@ -134,6 +134,9 @@ def test_product_refuses(q):
     assert bwd(w, _f(), None, 7, 4, _f(), _f(), 1 << 20, None) == 1   # unknown format
     assert bwd(w, None, x8(cols=32), 0, 4, _f(), _f(), 1 << 20, None) == 2   # rows of N are wanted
     assert bwd(w, None, None, 0, 0, None, None, 0, None) == 0
+    # rows in 8 bits bring their own format; the argument is ignored
+    assert bwd(w, None, x8(rows=0, cols=64), 7, 0, None, None, 0, None) == 0
+    assert bwd(w, None, x8(cols=64, fmt=7), 0, 4, _f(), _f(), 1 << 20, None) == 1
     assert q.qlora_fp8_workspace_bytes(0, 64, 32) == 0
     assert q.qlora_fp8_workspace_bytes(4, 64, 24) == 0
     assert q.qlora_fp8_workspace_bytes(4, 64, 32) >= 4 * (64 + 4)

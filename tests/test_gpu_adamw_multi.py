@@ -168,6 +168,12 @@ def test_refusals_padding_and_streams(q):
     moved.masters[0].data = moved.masters[0].clone()
     with pytest.raises(ValueError):
         q.qlora_adamw_multi(moved, grads, 1)
+    # a state put in the place of the group's own (it would not be the one that is updated)
+    for name, bits in (("m", 8), ("v_scales", 8), ("v", 32)):
+        put = q.AdamWGroup([p.clone() for p in masters], bits=bits)
+        setattr(put, name, getattr(put, name).clone())
+        with pytest.raises(ValueError):
+            q.qlora_adamw_multi(put, grads, 1)
 
 
 @pytest.mark.parametrize("bits", [8, 32])
