@@ -21,15 +21,21 @@
 // MN-major for dX (W_MN), whose reduction runs along N. In both a stage holds
 // 128 rows of 128 bytes in the 128-byte swizzle.
 //
-// Measured, 4096 rows x 11008 outputs x 4096: 195 us, 1.90 PFLOP/s, at the
-// board's 1000 W limit (SM clock 1.6 of 1.965 GHz); dX of the same weight 205 us
-// with the rows' quantizer. The chain from one use of a buffer to the next
-// (commit, barrier, reading back, barrier) is what shorter inputs wait for: 1024
-// rows x 4096 x 4096 take 18.9 us. On the way: scales read by the epilogue warps
-// themselves 275 us; sixteen epilogue warps and one line of shared memory a
-// scale 222; eight with 216 registers 211; barrier waits taken ahead 198. Halves
-// of 128 outputs with four buffers shortened no time (220: the operands are read
-// twice), nor did one barrier arrival a CTA instead of one a warp (229).
+// Measured, 4096 rows x 11008 outputs x 4096: 190 us, 1.95 PFLOP/s, at the
+// board's 1000 W limit (SM clock 1.6 of 1.965 GHz; single launches with pauses
+// 168 us); dX of the same weight 200 us with the rows' quantizer. A block takes
+// some 890 cycles: its sums are ready 740 after the issue (512 of them MMA),
+// the epilogue warps then take 450 to read them back and free the buffer, and
+// with two buffers the tensor core waits for that. The FMAs are a third of it
+// (taken out in a copy: 690 cycles, where the operands' way from L2, 50 bytes a
+// clock and SM, is the next bound). On the way: scales read by the epilogue
+// warps themselves 275 us; sixteen epilogue warps and one line of shared memory a
+// scale 222; eight with 216 registers 211; barrier waits taken ahead 192; a
+// chunk's scales read at once 190. Not kept, all slower: tiles of 160 outputs
+// with three buffers (206, dX 232) and of 192 with twelve epilogue warps (213):
+// more operand bytes an output; halves of 128 outputs with four buffers (220);
+// 32 columns a load, the next block's first ones requested ahead (195); one
+// barrier arrival a CTA instead of one a warp (229).
 //
 // Warps of a CTA (384 threads): 0 TMA; 1 tensor-memory allocation and, in the
 // even CTA, the MMA issue; 2-3 scales; 4-11 epilogue (lane quarter = warp % 4,
@@ -50,10 +56,12 @@ constexpr int kFp8PairIssueRegs = 56, kFp8PairEpiRegs = 216;
 // 384 threads are launched with at most 168 registers each
 static_assert(128 * kFp8PairIssueRegs + 256 * kFp8PairEpiRegs <= 384 * 168, "registers of the launch");
 constexpr int kFp8PairBoxes = 8 * 4 * 2048;  // four 32 x 32 bf16 output boxes an epilogue warp
-// scales: two chunks of eight reduction blocks, each block 128 rows' and two
-// weight blocks' (132 words: a warp's transposed stores spread over the banks)
-constexpr int kScaleChunk = 8, kScaleStride = 132;
-constexpr int kFp8PairRing = 2 * kScaleChunk * kScaleStride * 4;
+// scales: two chunks of eight reduction blocks, each 128 rows of eight (48
+// bytes apart: eight lanes' 16-byte loads then take all banks) and two weight
+// blocks' eight
+constexpr int kScaleChunk = 8, kScaleRow = 48;
+constexpr int kScaleBytes = 128 * kScaleRow + 2 * 4 * kScaleChunk;
+constexpr int kFp8PairRing = 2 * kScaleBytes;
 constexpr int kFp8PairSmem = kFp8PairStages * 32768 + kFp8PairBoxes + kFp8PairRing + 1024 + 256;
 
 
@@ -206,12 +214,12 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
     int tile = pair, k0 = 0;
     request(tile, k0);
     while (tile < ntiles && !__any_sync(0xFFFFFFFFu, *abort_flag)) {
-      const uint32_t slot = ring + (c * kScaleChunk + kl) * (kScaleStride * 4);
+      const uint32_t slot = ring + c * kScaleBytes + 4 * kl;
       if (!fp8_token(bar_se(c), cph)) fp8_wait(bar_se(c), cph, ab, QLORA_DEV_TIMEOUT_PRODUCER);
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sts32(slot + 4 * (64 * half + rl + 4 * j), __float_as_uint(v[j]));
-      if (rl == 0) sts32(slot + 4 * (128 + half), __float_as_uint(w));
+      for (int j = 0; j < 16; ++j) sts32(slot + (64 * half + rl + 4 * j) * kScaleRow, __float_as_uint(v[j]));
+      if (rl == 0) sts32(slot + 128 * kScaleRow + 4 * kScaleChunk * half, __float_as_uint(w));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sf(c));
       c ^= 1;
@@ -230,7 +238,8 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
     const uint32_t acce_even0 = mapa_shared(bar_acce(0), 0);
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * half;
     const uint32_t box = boxes + (warp - 4) * 8192;
-    const uint32_t ring_x = ring + 4 * (32 * quarter + lane), ring_w = ring + 4 * (128 + half);
+    const uint32_t ring_x = ring + (32 * quarter + lane) * kScaleRow;
+    const uint32_t ring_w = ring + 128 * kScaleRow + 4 * kScaleChunk * half;
     int b = 0, c = 0;              // accumulator buffer, scale chunk buffer
     uint32_t bph = 0, cph = 0;     // their parities
     bool ready = false;            // token of bar_accf(b)
@@ -241,48 +250,54 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      int left = 0;                // blocks left in the scale chunk
-      uint32_t slot = 0;
 #pragma unroll 1
-      for (int kb = p.kblocks; kb > 0; --kb) {
-        if (left == 0) {
-          if (!fp8_token(bar_sf(c), cph)) fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
-          __syncwarp();
-          left = min(kb, kScaleChunk);
-          slot = c * (kScaleChunk * kScaleStride * 4);
-        }
-        const float s = __uint_as_float(lds32(ring_x + slot)) * __uint_as_float(lds32(ring_w + slot));
-        const uint64_t s2 = f2(s, s);
-        slot += kScaleStride * 4;
-        if (--left == 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_se(c));
-          c ^= 1;
-          if (c == 0) cph ^= 1;
-        }
-        if (!ready) fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
+      for (int k0 = 0; k0 < p.kblocks; k0 += kScaleChunk) {
+        // the chunk's factors, all at once: a round trip through shared memory in
+        // every block would hold its sums up
+        if (!fp8_token(bar_sf(c), cph)) fp8_wait(bar_sf(c), cph, ab, QLORA_DEV_TIMEOUT_EPI);
         __syncwarp();
-        tc_fence_after();
-        const uint32_t t = tbase + b * 256;
-        const uint32_t acce = acce_even0 + 8u * b;
-        b ^= 1;
-        if (b == 0) bph ^= 1;
-        uint32_t ra[16], rb[16];
-        tmem_ld_32x32b_x16(t, ra);
-        tmem_ld_32x32b_x16(t + 16, rb);
+        float s[kScaleChunk];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          tc_wait_ld();
-          if (i == 6) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acce);
-            ready = fp8_token(bar_accf(b), bph);
+        for (int h = 0; h < kScaleChunk; h += 4) {
+          const float4 x = lds_f4(ring_x + c * kScaleBytes + 4 * h), w = lds_f4(ring_w + c * kScaleBytes + 4 * h);
+          s[h] = x.x * w.x;
+          s[h + 1] = x.y * w.y;
+          s[h + 2] = x.z * w.z;
+          s[h + 3] = x.w * w.w;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_se(c));
+        c ^= 1;
+        if (c == 0) cph ^= 1;
+#pragma unroll 1
+        for (int kb = min(p.kblocks - k0, kScaleChunk); kb > 0; --kb) {
+          const uint64_t s2 = f2(s[0], s[0]);
+#pragma unroll
+          for (int j = 0; j + 1 < kScaleChunk; ++j) s[j] = s[j + 1];
+          if (!ready) fp8_wait(bar_accf(b), bph, ab, QLORA_DEV_TIMEOUT_EPI);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t t = tbase + b * 256;
+          const uint32_t acce = acce_even0 + 8u * b;
+          b ^= 1;
+          if (b == 0) bph ^= 1;
+          uint32_t ra[16], rb[16];
+          tmem_ld_32x32b_x16(t, ra);
+          tmem_ld_32x32b_x16(t + 16, rb);
+          ready = fp8_token(bar_accf(b), bph);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            tc_wait_ld();
+            if (i == 6) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(acce);
+            }
+            promote16(acc + 8 * i, ra, s2);
+            if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 2), ra);
+            promote16(acc + 8 * (i + 1), rb, s2);
+            if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 3), rb);
           }
-          promote16(acc + 8 * i, ra, s2);
-          if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 2), ra);
-          promote16(acc + 8 * (i + 1), rb, s2);
-          if (i < 6) tmem_ld_32x32b_x16(t + 16 * (i + 3), rb);
         }
       }
       if (p.tma_out) {
