@@ -281,3 +281,14 @@ def test_captured_and_replayed(q, m):
         for _, out in graphs:
             assert torch.equal(out[0], want) and torch.equal(out[1], dx0)
     assert q.qlora_device_status() == (0, 0)
+
+
+def test_offsets_past_31_bits(q):
+    n, k = 11008, 128
+    m = 2 ** 31 // n + 300
+    w = q.qlora_quantize_fp8(torch.randn(n, k, device="cuda").bfloat16())
+    x = q.qlora_quantize_fp8_rows(torch.randn(m, k, device="cuda").bfloat16())
+    y = q.qlora_fp8_linear_fwd(w, x)
+    tail = q.FP8Rows(x.codes.view(torch.uint8)[-300:].clone().view(torch.float8_e4m3fn), x.scales[-300:].clone())
+    weight = w.codes.float() * w.scales.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)
+    _check_product(y[-300:], tail.dequantize().double().cpu().numpy(), weight.double().cpu().numpy())

@@ -195,3 +195,21 @@ def test_captured_and_on_another_stream(q):
         assert torch.equal(yy.codes.view(torch.uint8), want[0].codes.view(torch.uint8)) and torch.equal(yy.scales, want[0].scales)
         assert torch.equal(hh, want[1]) and torch.equal(rr, want[2])
         assert torch.equal(bb[0], bwant[0]) and torch.equal(bb[1], bwant[1])
+
+
+def test_offsets_past_31_bits(q):
+    d = 8192
+    rows = 2 ** 31 // d + 1300
+    x = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda").normal_()
+    gamma = torch.rand(d, device="cuda").bfloat16()
+    tail = x[-1300:].clone()
+    y, _, rstd = q.qlora_rmsnorm_fwd(x, gamma)
+    y8, _, _ = q.qlora_rmsnorm_fwd(x, gamma, fp8=True)
+    dx, _ = q.qlora_rmsnorm_bwd(y, x, gamma, rstd, want_dgamma=False)
+    # rows do not depend on one another (as many as take the same sum's order)
+    ty, _, trstd = q.qlora_rmsnorm_fwd(tail, gamma)
+    ty8, _, _ = q.qlora_rmsnorm_fwd(tail, gamma, fp8=True)
+    tdx, _ = q.qlora_rmsnorm_bwd(ty, tail, gamma, trstd, want_dgamma=False)
+    assert torch.equal(y[-1300:], ty) and torch.equal(rstd[-1300:], trstd) and torch.equal(dx[-1300:], tdx)
+    assert torch.equal(y8.codes[-1300:].view(torch.uint8), ty8.codes.view(torch.uint8))
+    assert torch.equal(y8.scales[-1300:], ty8.scales)
