@@ -18,6 +18,7 @@ Functions carry the C names:
     qlora_rmsnorm_bwd, qlora_adamw_multi
 """
 
+import array
 import ctypes
 import operator
 import os
@@ -814,6 +815,6 @@ def qlora_adamw_multi(group, grads, step, lr=1e-4, betas=(0.9, 0.999), eps=1e-8,
           list(map(T.data_ptr, group.params or ())) == group._at[1] and group._states() == group._states_at,
           "qlora_adamw_multi", "a master's, param's or state's storage has moved since the group was made")
     desc = group._desc.copy()
-    desc[:, 2] = list(map(T.data_ptr, grads))
+    desc[:, 2] = array.array("Q", map(T.data_ptr, grads))      # numpy takes its memory as it is
     hp = AdamwParams(lr, betas[0], betas[1], eps, weight_decay, step)
     _check(lib.qlora_adamw_multi(desc.ctypes.data, len(grads), group.bits, hp, _raw_stream(dev)), "qlora_adamw_multi")
