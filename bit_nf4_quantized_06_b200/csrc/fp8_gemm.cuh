@@ -61,6 +61,15 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, const Fp
   }
 }
 
+// For the one thread that issues MMAs: asks again at once, where a suspended
+// wait takes its time to wake (pair kernel, 1% of the time).
+__device__ __forceinline__ bool fp8_spin(uint32_t bar, uint32_t parity, const Fp8Abort& a, unsigned code) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (fp8_token(bar, parity)) return true;
+  return fp8_wait(bar, parity, a, code);
+}
+
 // Instruction descriptor for kind::f8f6f4: A e4m3 or e5m2, B e4m3, fp32 D.
 __device__ __forceinline__ uint32_t idesc_fp8(int m, int n, int a_format, bool b_mn_major) {
   return (1u << 4) | (static_cast<uint32_t>(a_format) << 7) | ((b_mn_major ? 1u : 0u) << 16) |

@@ -21,9 +21,9 @@
 // MN-major for dX (W_MN), whose reduction runs along N. In both a stage holds
 // 128 rows of 128 bytes in the 128-byte swizzle.
 //
-// Measured, 4096 rows x 11008 outputs x 4096: 190 us, 1.95 PFLOP/s, at the
+// Measured, 4096 rows x 11008 outputs x 4096: 189 us, 1.95 PFLOP/s, at the
 // board's 1000 W limit (SM clock 1.6 of 1.965 GHz; single launches with pauses
-// 168 us); dX of the same weight 200 us with the rows' quantizer. A block takes
+// 166 us); dX of the same weight 200 us with the rows' quantizer. A block takes
 // some 890 cycles: its sums are ready 740 after the issue (512 of them MMA),
 // the epilogue warps then take 450 to read them back and free the buffer, and
 // with two buffers the tensor core waits for that. The FMAs are a third of it
@@ -31,7 +31,7 @@
 // clock and SM, is the next bound). On the way: scales read by the epilogue
 // warps themselves 275 us; sixteen epilogue warps and one line of shared memory a
 // scale 222; eight with 216 registers 211; barrier waits taken ahead 192; a
-// chunk's scales read at once 190. Not kept, all slower: tiles of 160 outputs
+// chunk's scales read at once 190, the MMA's thread spinning 189. Not kept, all slower: tiles of 160 outputs
 // with three buffers (206, dX 232) and of 192 with twelve epilogue warps (213):
 // more operand bytes an output; halves of 128 outputs with four buffers (220);
 // 32 columns a load, the next block's first ones requested ahead (195); one
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
       const int64_t blocks = static_cast<int64_t>((ntiles - pair + npairs - 1) / npairs) * p.kblocks;
       for (int64_t i = 0; i < blocks; ++i) {
         if (!full && !fp8_wait(bar_full(s), ph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
-        if (!free && !fp8_wait(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
+        if (!free && !fp8_spin(bar_acce(b), aph, ab, QLORA_DEV_TIMEOUT_MMA)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + b * 256, accf = bar_accf(b), empty = bar_empty(s);
         const uint64_t dx = dx0 + s * (STAGE_BYTES >> 4), dw = dw0 + s * (STAGE_BYTES >> 4);
