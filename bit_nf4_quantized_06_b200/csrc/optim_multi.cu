@@ -6,18 +6,26 @@
 // the CTAs walk the chunks of all tensors as one list.
 //
 // 8 bits: m and sqrt(v) are e4m3 codes with one fp32 scale per 256 values of
-// a tensor (fp8_dev.cuh); a warp owns a block, eight values a lane, so that
+// a tensor; a warp owns a block, eight values a lane, so that
 // the block's maxima are warp shuffles. sqrt(v) rather than v: e4m3 spans
 // 2^17.8 from its smallest code to its largest, which is 2^35 of v. A code of
 // a value above zero is not allowed to become zero, else the next step would
 // divide by eps alone. The step uses the new m and v in fp32, so rounding
 // them to 8 bits acts on later steps only.
 //
+// The states are defined operation by operation (the header has the list), so
+// that a state after any number of steps is one set of bits: a value that a
+// last bit moved over a rounding border would be a whole code away, and as its
+// block's next largest value would move the scale by some per cent. With m in
+// one fused operation 3 of 4 runs of four steps over 160 million values ended
+// with such a block. amax / 448 and 448 / amax are products with a
+// reciprocal, as torch's operators on a tensor and a number are on the GPU.
+//
 // Bound by HBM: 30 bytes a value (32 bits, with the bf16 copy) or 18.1 (8
 // bits). A CTA takes chunks of eight blocks, a block a warp, through a ring of
 // stages in shared memory: one stage holds a chunk's master values, gradients
 // and states, filled by four bulk copies that are requested several chunks
-// ahead. Measured, 8 bits, 160 million values in 448 tensors: 457 us, 6.3 TB/s
+// ahead. Measured, 8 bits, 160 million values in 448 tensors: 466 us, 6.2 TB/s
 // (loads to registers kept 61 KB in flight on an SM, 573 us; a ring a warp, of
 // 256-byte copies, was bound by the copies' number, 816 us); 32 bits, 134
 // million values: 688 us, 5.9 TB/s.
@@ -66,11 +74,6 @@ struct Multi {
 constexpr int kCapSmall = 24, kCapLarge = 470;
 static_assert(sizeof(Multi<kCapLarge>) <= 32764, "kernel parameter block");
 
-__device__ __forceinline__ float sqrt_approx(float v) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -85,6 +88,14 @@ __device__ __forceinline__ float hi_of(uint64_t v) {
   uint32_t a, b;
   f2_split(v, a, b);
   return __uint_as_float(b);
+}
+
+// a x + b y in pairs, each product and the sum rounded by itself. The assembler
+// joins a packed product and a packed sum into one fused operation, `.rn` or
+// not; these scalar forms it leaves as they are.
+__device__ __forceinline__ uint64_t sum_apart(uint64_t a, uint64_t x, uint64_t b, uint64_t y) {
+  return f2(__fadd_rn(__fmul_rn(lo_of(a), lo_of(x)), __fmul_rn(lo_of(b), lo_of(y))),
+            __fadd_rn(__fmul_rn(hi_of(a), hi_of(x)), __fmul_rn(hi_of(b), hi_of(y))));
 }
 
 // Constants of the 8-bit step, in pairs.
@@ -107,10 +118,13 @@ struct Stage {
 __device__ __forceinline__ int value_of(int lane, int j) { return (j >> 2) * 128 + 4 * lane + (j & 3); }
 
 // The 8-bit step of the block at i0 (`src`: its stage, or 0 for plain
-// accesses; `read` is called once its values are in registers), in packed pairs, with the hardware's square root and reciprocal (off by a step
-// or two of fp32, far below a code's own rounding and below p's in the
-// update): with the exact ones this kernel was bound by issue (83
-// instructions a value, 654 us for 160 million values).
+// accesses; `read` is called once its values are in registers), in packed
+// pairs. The states' operations are rounded one by one (the square root's share
+// is 22 us of 466 for 160 million values; with the hardware's approximate one
+// states were not reproducible). The update's reciprocal, which no state
+// depends on, is the hardware's, off by one step of fp32 at most: with a
+// rounded quotient too this kernel was bound by issue (83 instructions a value,
+// 654 us).
 template <typename Read>
 __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, const Stage& src, const Hyper2& hp,
                                       Read read) {
@@ -153,11 +167,11 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
     const float2 mm = fp8_unpack2<kE4M3>((j < 4 ? mq.x : mq.y) >> sh);
     const float2 rr = fp8_unpack2<kE4M3>((j < 4 ? vq.x : vq.y) >> sh);
     const uint64_t g2 = f2(g[j], g[j + 1]);
-    const uint64_t m2 = f2_fma(hp.beta1, f2_mul(f2(mm.x, mm.y), ms2), f2_mul(hp.gain1, g2));
+    const uint64_t m2 = sum_apart(hp.beta1, f2_mul(f2(mm.x, mm.y), ms2), hp.gain1, g2);
     const uint64_t r2 = f2_mul(f2(rr.x, rr.y), vs2);
-    const uint64_t v2 = f2_fma(hp.beta2, f2_mul(r2, r2), f2_mul(f2_mul(hp.gain2, g2), g2));
-    r[j] = sqrt_approx(lo_of(v2));
-    r[j + 1] = sqrt_approx(hi_of(v2));
+    const uint64_t v2 = sum_apart(hp.beta2, f2_mul(r2, r2), hp.gain2, f2_mul(g2, g2));
+    r[j] = __fsqrt_rn(lo_of(v2));
+    r[j + 1] = __fsqrt_rn(hi_of(v2));
     const uint64_t d2 = f2_fma(f2(r[j], r[j + 1]), hp.inv_sqrt_bc2, hp.eps);
     const uint64_t q2 = f2_mul(m2, f2(rcp_approx(lo_of(d2)), rcp_approx(hi_of(d2))));
     const uint64_t p2 = f2_fma(hp.neg_step, q2, f2_mul(f2(p[j], p[j + 1]), hp.decay));
@@ -191,7 +205,7 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
   constexpr float F = 448.0f;
   am = fmaxf(am, kFp8Least);
   av = fmaxf(av, kFp8Least);
-  const float im = F / am, iv = F / av;
+  const float im = F * __frcp_rn(am), iv = F * __frcp_rn(av);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     m[j] *= im;
@@ -202,7 +216,7 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
   vq = make_uint2(fp8_pack4<kE4M3>(r[0], r[1], r[2], r[3]), fp8_pack4<kE4M3>(r[4], r[5], r[6], r[7]));
   if (lane < 2) {
     float* scale = lane == 0 ? t.m_scales : t.v_scales;
-    scale[blk] = (lane == 0 ? am : av) / F;
+    scale[blk] = (lane == 0 ? am : av) * (1.0f / F);
   }
   if (src.p != 0) {
 #pragma unroll

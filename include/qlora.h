@@ -403,13 +403,21 @@ QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void *dy_bf16, const void *h_bf
  * adapters and norm gains of a model), with states in 32 bits or in 8.
  *   state_bits 32: m, v fp32 [n]; m_scales, v_scales unused.
  *   state_bits 8:  m holds e4m3 codes [n] of m and v e4m3 codes [n] of
- *     sqrt(v), quantized as above in blocks of 256 consecutive values of the
- *     tensor (scales [ceil(n/256)] each; all zero bytes mean zero states). A
- *     sqrt(v) above zero keeps a code above zero (at least 2^-9), so that no
+ *     sqrt(v) in blocks of 256 consecutive values of the tensor (scales
+ *     [ceil(n/256)] each; all zero bytes mean zero states). The states are
+ *     these fp32 operations, each rounded by itself (none fused), so that any
+ *     implementation gets the same bits after any number of steps:
+ *       m = b1 * (code * scale) + (1 - b1) * g
+ *       r = code * scale;  v = b2 * (r * r) + (1 - b2) * (g * g);  r = sqrt(v)
+ *       amax  = max over the block's finite |m| (or r), at least 2^-100
+ *       scale = amax * fl32(1 / 448)
+ *       code  = e4m3_rn(clamp(value * (448 * fl32(1 / amax)), -448, 448))
+ *     A root above zero keeps a code above zero (at least 2^-9), so that no
  *     step divides by eps alone. The root halves the exponent range that v
  *     needs. A gradient that is not finite spoils its own value only, as with
- *     32-bit states. The step itself uses the new m and v before they are
- *     rounded to 8 bits.
+ *     32-bit states: its codes are NaN and stay out of amax. The step itself
+ *     uses the new m and r before they are rounded to 8 bits; its quotient
+ *     m / (r / sqrt(1 - b2^t) + eps) is off by 2^-21 of itself at most.
  * `tensors` is a host array; it is read during the call (a captured call
  * keeps the pointers and the step number that it was captured with) and may
  * be reused at once. All buffers are device memory (states in pinned host

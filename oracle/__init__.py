@@ -33,6 +33,7 @@ Modules
 ``fp8``     8-bit floating point (e4m3, e5m2) and its block quantization.
 ``norm``    RMS norm and its gradients in fp64.
 ``optim``   AdamW in fp64.
+``adamw8``  the 8-bit AdamW's states, operation by operation in fp32.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test
 against something other than itself (closed forms, brute force, finite
