@@ -11,7 +11,7 @@ Functions carry the C names:
     qlora_nf4_bytes, qlora_nf4_codebook, qlora_quantize_nf4, qlora_dequantize,
     qlora_workspace_bytes, qlora_fwd_workspace_bytes, qlora_linear_fwd, qlora_linear_fwd_ex,
     qlora_linear_fwd_noalloc, qlora_linear_bwd, qlora_device_status, qlora_status_string, qlora_version,
-    qlora_launch_count, qlora_selftest_wait_timeout, qlora_merge_lora, qlora_adamw_step, qlora_adamw_host,
+    qlora_launch_count, qlora_selftest_wait_timeout, qlora_selftest_ring_timeout, qlora_merge_lora, qlora_adamw_step, qlora_adamw_host,
     qlora_adamw_paged, qlora_adamw_staged, qlora_set_gemm_schedule, qlora_get_gemm_schedule,
     qlora_quantize_fp8, qlora_dequantize_fp8, qlora_quantize_fp8_rows, qlora_fp8_workspace_bytes,
     qlora_fp8_linear_fwd, qlora_fp8_linear_bwd, qlora_rmsnorm_fwd, qlora_rmsnorm_workspace_bytes,
@@ -29,7 +29,8 @@ __all__ = [
     "qlora_workspace_bytes", "qlora_fwd_workspace_bytes", "qlora_linear_fwd", "qlora_linear_fwd_ex", "qlora_linear_fwd_noalloc",
     "qlora_linear_bwd",
     "qlora_device_status", "qlora_status_string", "qlora_version", "qlora_launch_count",
-    "qlora_selftest_wait_timeout", "qlora_merge_lora", "qlora_adamw_step", "qlora_adamw_host", "qlora_adamw_paged",
+    "qlora_selftest_wait_timeout", "qlora_selftest_ring_timeout", "SELFTEST_RING_NEVER", "SELFTEST_RING_LATE",
+    "SELFTEST_RING_ONE", "qlora_merge_lora", "qlora_adamw_step", "qlora_adamw_host", "qlora_adamw_paged",
     "qlora_adamw_staged", "qlora_set_gemm_schedule", "qlora_get_gemm_schedule",
     "AdamwParams",
     "FP8_E4M3", "FP8_E5M2", "FP8Weight", "FP8Rows", "Fp8Struct", "Fp8RowsStruct", "qlora_quantize_fp8",
@@ -118,6 +119,8 @@ lib.qlora_merge_lora.argtypes = [_P(Nf4Struct), _vp, _vp, _i32, _f32, _vp, _vp]
 lib.qlora_merge_lora.restype = ctypes.c_int
 lib.qlora_selftest_wait_timeout.argtypes = [ctypes.c_uint32, _vp]
 lib.qlora_selftest_wait_timeout.restype = ctypes.c_int
+lib.qlora_selftest_ring_timeout.argtypes = [ctypes.c_uint32, _i32, _vp, _vp]
+lib.qlora_selftest_ring_timeout.restype = ctypes.c_int
 lib.qlora_launch_count.argtypes = []
 lib.qlora_launch_count.restype = ctypes.c_uint64
 lib.qlora_set_gemm_schedule.argtypes = [ctypes.c_int32]
@@ -346,6 +349,20 @@ def qlora_selftest_wait_timeout(limit_us, stream=None):
     """Launch the bounded-wait self test (a wait that nothing completes); the
     timeout shows up in the next qlora_device_status()."""
     _check(lib.qlora_selftest_wait_timeout(int(limit_us), _stream_ptr(stream)), "qlora_selftest_wait_timeout")
+
+
+SELFTEST_RING_NEVER, SELFTEST_RING_LATE, SELFTEST_RING_ONE = 0, 1, 2
+
+
+def qlora_selftest_ring_timeout(limit_us, mode, out, stream=None):
+    """Launch the self test of a ring of bulk copies whose wait gives up; `out`
+    (int32 CUDA tensor of 129) gets the landings each thread saw and whether
+    every copy landed before the kernel ended."""
+    torch = _torch()
+    if out.dtype is not torch.int32 or out.shape != (129,) or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("qlora_selftest_ring_timeout: out must be a contiguous int32 CUDA tensor of 129")
+    _check(lib.qlora_selftest_ring_timeout(int(limit_us), int(mode), out.data_ptr(), _stream_ptr(stream)),
+           "qlora_selftest_ring_timeout")
 
 
 def qlora_merge_lora(q, a, b, alpha, out=None, stream=None):

@@ -1199,6 +1199,17 @@ qlora_status_t qlora_selftest_wait_timeout(uint32_t limit_us, void* stream) {
   return launch_status();
 }
 
+qlora_status_t qlora_selftest_ring_timeout(uint32_t limit_us, int32_t mode, uint32_t* out, void* stream) {
+  if (out == nullptr || mode < QLORA_SELFTEST_RING_NEVER || mode > QLORA_SELFTEST_RING_ONE)
+    return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(out)) return QLORA_ERR_ALIGNMENT;
+  qlora_status_t s = device_ready(nullptr);
+  if (s != QLORA_OK) return s;
+  const uint64_t us = std::min<uint64_t>(std::max<uint32_t>(limit_us, 1u), 2000000u);
+  k_selftest_ring<<<1, 128, 0, static_cast<cudaStream_t>(stream)>>>(us * 1000ull, mode, out);
+  return launch_status();
+}
+
 qlora_status_t qlora_device_status(void* stream, uint32_t* bits) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QLORA_ERR_CUDA;
   unsigned int v = 0;

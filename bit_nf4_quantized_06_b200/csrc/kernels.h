@@ -193,6 +193,7 @@ constexpr int tc_pair_smem_bytes(int nh) {
 __global__ void k_reduce_splits(SmallParams p);
 
 __global__ void k_selftest_wait(uint64_t limit_ns);
+__global__ void k_selftest_ring(uint64_t limit_ns, int mode, uint32_t* out);
 
 // LoRA merge for export: out = bf16(W_hat + s B A), 128 x 128 tiles.
 struct MergeParams {

@@ -334,7 +334,7 @@ template <int NV, bool VEC, bool BULK>
 __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   extern __shared__ __align__(16) uint8_t s_dyn[];   // BULK: the stages; then d floats for the groups' dgamma
   __shared__ float s_red[2][16 * 16];
-  __shared__ __align__(8) uint64_t s_bar[16 * kBwdMaxStages];
+  __shared__ __align__(8) uint64_t s_bar[16 * ring_words(kBwdMaxStages)];
   static_assert(!BULK || (VEC && NV > 0), "bulk copies are for whole rows in registers");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   constexpr int KEEP = NV > 0 ? NV : 1;
@@ -346,17 +346,14 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   const uint32_t row_bytes = static_cast<uint32_t>(width) * 2;
   const int parts = p.dres != nullptr ? 3 : 2;
   const uint32_t stage_bytes = 3 * row_bytes;
-  const uint32_t ring = smem_u32(s_dyn) + threadIdx.y * p.stages * stage_bytes;
-  const uint32_t bars = smem_u32(s_bar) + threadIdx.y * kBwdMaxStages * 8;
+  const uint32_t base = smem_u32(s_dyn) + threadIdx.y * p.stages * stage_bytes;
+  BulkRing ring(smem_u32(s_bar) + threadIdx.y * ring_words(kBwdMaxStages) * 8);
   uint64_t acc[KEEP][4];
 #pragma unroll
   for (int v = 0; v < KEEP; ++v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[v][i] = 0;
-  if (BULK && one) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(bars + 8 * s, 1);
-    fence_mbar_init();
-  }
+  if (BULK && one) ring.init(p.stages);
   if (BULK) __syncthreads();
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -365,9 +362,9 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.y;
   auto fill = [&](int64_t row, int stage) {          // one thread of the group
-    if (row >= p.rows) return;
-    const uint32_t bar = bars + 8 * stage, dst = ring + stage * stage_bytes;
-    mbar_arrive_expect_tx(bar, parts * row_bytes);
+    if (row >= p.rows || ring.given_up()) return;
+    const uint32_t bar = ring.bar(stage), dst = base + stage * stage_bytes;
+    ring.expect(stage, parts * row_bytes);
     bulk_load(dst, p.dy + row * p.d, row_bytes, bar);
     bulk_load(dst + row_bytes, p.h + row * p.d, row_bytes, bar);
     if (parts == 3) bulk_load(dst + 2 * row_bytes, p.dres + row * p.d, row_bytes, bar);
@@ -381,7 +378,6 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
   }
 
   int stage = 0, turn = 0;
-  uint32_t phase = 0;
   float next_rstd = row0 < p.rows ? p.rstd[row0] : 0.0f;
   for (int64_t row = row0; row < p.rows; row += stride) {
     const int d = width;
@@ -391,9 +387,9 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
     if (row + stride < p.rows) next_rstd = p.rstd[row + stride];
     uint4 kdy[KEEP], kh[KEEP], kres[KEEP];
     float dot = 0.0f;
-    const uint32_t src = ring + stage * stage_bytes;
+    const uint32_t src = base + stage * stage_bytes;
     if constexpr (BULK) {
-      if (!bulk_wait(bars + 8 * stage, phase)) return;
+      ring.wait(stage);                 // given up on: this and the later rows are void, the barriers are met
     } else if constexpr (NV > 0) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -468,11 +464,9 @@ __global__ void __launch_bounds__(512, 1) k_rmsnorm_bwd(NormBwd p) {
         }
       }
     }
-    if (BULK && ++stage == p.stages) {
-      stage = 0;
-      phase ^= 1;
-    }
+    if (BULK && ++stage == p.stages) stage = 0;
   }
+  if (BULK && one) ring.drain();
   if constexpr (NV > 0) {
     if (prow == nullptr) return;
     float* s_part = reinterpret_cast<float*>(s_dyn);

@@ -93,19 +93,20 @@ __device__ __forceinline__ float hi_of(uint64_t v) {
 // a x + b y in pairs, each product and the sum rounded by itself. The assembler
 // joins a packed product and a packed sum into one fused operation, `.rn` or
 // not; these scalar forms it leaves as they are.
-__device__ __forceinline__ uint64_t sum_apart(uint64_t a, uint64_t x, uint64_t b, uint64_t y) {
-  return f2(__fadd_rn(__fmul_rn(lo_of(a), lo_of(x)), __fmul_rn(lo_of(b), lo_of(y))),
-            __fadd_rn(__fmul_rn(hi_of(a), hi_of(x)), __fmul_rn(hi_of(b), hi_of(y))));
+__device__ __forceinline__ uint64_t sum_apart(float a, uint64_t x, float b, uint64_t y) {
+  return f2(__fadd_rn(__fmul_rn(a, lo_of(x)), __fmul_rn(b, lo_of(y))),
+            __fadd_rn(__fmul_rn(a, hi_of(x)), __fmul_rn(b, hi_of(y))));
 }
 
-// Constants of the 8-bit step, in pairs.
+// Constants of the 8-bit step; the update's in pairs.
 struct Hyper2 {
-  uint64_t beta1, gain1, beta2, gain2, decay, neg_step, inv_sqrt_bc2, eps;
+  float beta1, gain1, beta2, gain2;
+  uint64_t decay, neg_step, inv_sqrt_bc2, eps;
 };
 __device__ __forceinline__ Hyper2 hyper2(const AdamwHyper& a) {
   auto two = [](float v) { return f2(v, v); };
-  return Hyper2{two(a.beta1), two(1.0f - a.beta1), two(a.beta2), two(1.0f - a.beta2), two(a.decay),
-                two(-a.step_size), two(a.inv_sqrt_bc2), two(a.eps)};
+  return Hyper2{a.beta1,      1.0f - a.beta1,      a.beta2,           1.0f - a.beta2,
+                two(a.decay), two(-a.step_size), two(a.inv_sqrt_bc2), two(a.eps)};
 }
 
 // Where a block's values lie in a stage; p == 0: nowhere.
@@ -118,8 +119,8 @@ struct Stage {
 __device__ __forceinline__ int value_of(int lane, int j) { return (j >> 2) * 128 + 4 * lane + (j & 3); }
 
 // The 8-bit step of the block at i0 (`src`: its stage, or 0 for plain
-// accesses; `read` is called once its values are in registers), in packed
-// pairs. The states' operations are rounded one by one (the square root's share
+// accesses; `read` is called once its values are in registers, and says whether
+// they may be used), in packed pairs. The states' operations are rounded one by one (the square root's share
 // is 22 us of 466 for 160 million values; with the hardware's approximate one
 // states were not reproducible). The update's reciprocal, which no state
 // depends on, is the hardware's, off by one step of fp32 at most: with a
@@ -157,7 +158,7 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
     mq = make_uint2(mb[0] | mb[1] << 8 | mb[2] << 16 | mb[3] << 24, mb[4] | mb[5] << 8 | mb[6] << 16 | mb[7] << 24);
     vq = make_uint2(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24, vb[4] | vb[5] << 8 | vb[6] << 16 | vb[7] << 24);
   }
-  read();
+  if (!read()) return;
   const uint64_t ms2 = f2(ms, ms), vs2 = f2(vs, vs);
   float m[8], r[8];
   float am = 0.0f, av = 0.0f;
@@ -269,7 +270,7 @@ __device__ __forceinline__ void step32(const MultiTensor& t, int64_t i0, int lan
       v[j] = ok ? vs[c] : 0.0f;
     }
   }
-  read();
+  if (!read()) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) p[j] = adamw_update(p[j], g[j], m[j], v[j], root, hp);
   if (src.p != 0) {
@@ -302,15 +303,13 @@ constexpr int stage_bytes(bool b8) { return kChunk * (b8 ? 10 : 16); }
 template <int CAP, bool BITS8>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw_multi(const __grid_constant__ Multi<CAP> a) {
   extern __shared__ __align__(128) uint8_t s_ring[];
-  __shared__ __align__(8) uint64_t s_bar[kStages];
+  __shared__ __align__(8) uint64_t s_bar[ring_words(kStages)];
   constexpr uint32_t W = BITS8 ? 1 : 4;          // bytes of a state
   constexpr uint32_t STAGE = stage_bytes(BITS8);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t ring = smem_u32(s_ring), bars = smem_u32(s_bar);
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
-    fence_mbar_init();
-  }
+  const uint32_t base = smem_u32(s_ring);
+  BulkRing ring(smem_u32(s_bar));
+  if (threadIdx.x == 0) ring.init(kStages);
   __syncthreads();
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -328,11 +327,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_multi(const __grid_consta
     return a.first[c.t] < 0 && static_cast<int64_t>(c.chunk - first(c.t) + 1) * kChunk <= a.t[c.t].n;
   };
   auto request = [&](const Cursor& c, int s) {   // one thread
-    if (c.chunk >= a.chunks || !whole(c)) return;
+    if (c.chunk >= a.chunks || !whole(c) || ring.given_up()) return;
     const MultiTensor& t = a.t[c.t];
     const int64_t i0 = static_cast<int64_t>(c.chunk - first(c.t)) * kChunk;
-    const uint32_t dst = ring + s * STAGE, bar = bars + 8 * s;
-    mbar_arrive_expect_tx(bar, STAGE);
+    const uint32_t dst = base + s * STAGE, bar = ring.bar(s);
+    ring.expect(s, STAGE);
     bulk_load(dst, t.master + i0, kChunk * 4, bar);
     bulk_load(dst + kChunk * 4, t.grad + i0, kChunk * 4, bar);
     bulk_load(dst + kChunk * 8, static_cast<const uint8_t*>(t.m) + i0 * W, kChunk * W, bar);
@@ -359,16 +358,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_multi(const __grid_consta
     }
   }
   int s = 0;
-  uint32_t phases = 0;         // one bit a stage; it turns when the stage was filled
   for (; cur.chunk < a.chunks; cur.chunk += stride) {
     settle(cur);
     const MultiTensor& t = a.t[cur.t];
     const int64_t i0 = static_cast<int64_t>(cur.chunk - first(cur.t)) * kChunk + warp * kStateBlock;
     Stage src{0, 0, 0, 0};
+    bool ok = true;
     if (whole(cur)) {
-      if (!bulk_wait(bars + 8 * s, (phases >> s) & 1)) return;
-      phases ^= 1u << s;
-      const uint32_t at = ring + s * STAGE;
+      ok = ring.wait(s);
+      const uint32_t at = base + s * STAGE;
       src = Stage{at + warp * 1024, at + kChunk * 4 + warp * 1024, at + kChunk * 8 + warp * (kStateBlock * W),
                   at + kChunk * (8 + W) + warp * (kStateBlock * W)};
     }
@@ -379,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_multi(const __grid_consta
         request(ahead, s);
         ahead.chunk += stride;
       }
+      return __all_sync(0xFFFFFFFFu, ok);   // a warp whose copies did not land in time writes nothing
     };
     if (i0 >= t.n)
       read();
@@ -388,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_multi(const __grid_consta
       step32(t, i0, lane, src, a.hp, read);
     s = s + 1 == kStages ? 0 : s + 1;
   }
+  if (threadIdx.x == 0) ring.drain();
 }
 
 using host::aligned;

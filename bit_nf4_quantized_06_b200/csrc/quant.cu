@@ -23,9 +23,11 @@
 // 8-weight chunk is encoded and written back as one 32-bit word, again
 // coalesced. W is read exactly once; codes, scale codes and s_max are
 // written exactly once.
+#include "bulk.cuh"
 #include "ptx.cuh"
 #include "nf4_dev.cuh"
 #include "kernels.h"
+#include "../../include/qlora.h"
 
 namespace qlora {
 
@@ -347,6 +349,45 @@ __global__ void __launch_bounds__(32) k_selftest_wait(uint64_t limit_ns) {
       }
     }
   }
+}
+
+// The same for a ring of bulk copies (bulk.cuh): one CTA, a ring of two stages
+// over eight rounds, of which round 3's copy does not come in time. Every wait
+// and the drain are bounded by `limit_ns`; every thread meets every barrier.
+// out[thread]: the rounds whose copies the thread saw land; out[128]: whether
+// the drain saw every copy land.
+__global__ void __launch_bounds__(128) k_selftest_ring(uint64_t limit_ns, int mode, uint32_t* out) {
+  constexpr int STAGES = 2, ROUNDS = 8;
+  constexpr uint32_t BYTES = 128 * 4;       // out's own first words, whatever they hold
+  __shared__ __align__(16) uint8_t s_stage[STAGES][BYTES];
+  __shared__ __align__(8) uint64_t s_bar[ring_words(STAGES)];
+  BulkRing ring(smem_u32(s_bar));
+  if (threadIdx.x == 0) ring.init(STAGES);
+  __syncthreads();
+  auto fill = [&](int round) {
+    if (round >= ROUNDS || ring.given_up()) return;
+    const int s = round % STAGES;
+    ring.expect(s, BYTES);
+    if (round != 3 || mode == QLORA_SELFTEST_RING_ONE) bulk_load(smem_u32(s_stage[s]), out, BYTES, ring.bar(s));
+  };
+  if (threadIdx.x == 0)
+    for (int r = 0; r < STAGES; ++r) fill(r);
+  uint32_t landed = 0;
+  for (int r = 0; r < ROUNDS; ++r) {
+    if (mode == QLORA_SELFTEST_RING_ONE && r == 2 && threadIdx.x == 5)
+      ring.give_up(QLORA_DEV_TIMEOUT_SELFTEST);        // while the copy lands for the others
+    else
+      landed += ring.wait(r % STAGES, limit_ns, QLORA_DEV_TIMEOUT_SELFTEST);
+    __syncthreads();
+    if (threadIdx.x == 0) fill(r + STAGES);
+  }
+  if (threadIdx.x == 0) {
+    if (mode == QLORA_SELFTEST_RING_LATE) bulk_load(smem_u32(s_stage[1]), out, BYTES, ring.bar(1));
+    const bool ok = ring.drain(limit_ns);
+    out[128] = ok;
+  }
+  __syncthreads();                          // the copies from `out` are over
+  out[threadIdx.x] = landed;
 }
 
 }  // namespace qlora

@@ -450,7 +450,7 @@ QLORA_API qlora_status_t qlora_device_status(void *stream, uint32_t *bits);
 #define QLORA_STATUS_BIT_MMA      0x2u  /* the MMA issuer waited for operands      */
 #define QLORA_STATUS_BIT_RESTORE  0x4u  /* a restore warp waited for codes/scales  */
 #define QLORA_STATUS_BIT_EPILOGUE 0x8u  /* the epilogue waited for an accumulator  */
-#define QLORA_STATUS_BIT_SELFTEST 0x10u /* qlora_selftest_wait_timeout             */
+#define QLORA_STATUS_BIT_SELFTEST 0x10u /* the qlora_selftest_* diagnostics        */
 
 /* Diagnostic for the failure-detection path (not part of the method): one
  * tiny kernel waits on a shared-memory barrier that nothing ever completes,
@@ -460,6 +460,23 @@ QLORA_API qlora_status_t qlora_device_status(void *stream, uint32_t *bits);
  * Lets a caller check that its error handling sees a timed-out wait without
  * any GPU fault. */
 QLORA_API qlora_status_t qlora_selftest_wait_timeout(uint32_t limit_us, void *stream);
+
+/* The same for a ring of bulk copies, as the RMS norm's gradient and the
+ * many-tensor AdamW use them: one CTA of 128 threads goes through eight
+ * rounds of a two-stage ring in which a wait gives up after limit_us (clamped
+ * as above). No thread leaves before the others, no copy is requested after
+ * the give-up, and copies under way land before the kernel ends.
+ *   NEVER: round 3's copy is announced and never made; the drain gives up too.
+ *   LATE:  it is made after every thread gave up on it.
+ *   ONE:   one thread gives up in round 2 while the copy lands for the others.
+ * out (device, 129 words, 16-byte aligned): how many rounds' copies each
+ * thread saw land, then 1 if the drain saw all of them land, else 0. */
+typedef enum {
+  QLORA_SELFTEST_RING_NEVER = 0,
+  QLORA_SELFTEST_RING_LATE = 1,
+  QLORA_SELFTEST_RING_ONE = 2
+} qlora_selftest_ring_t;
+QLORA_API qlora_status_t qlora_selftest_ring_timeout(uint32_t limit_us, int32_t mode, uint32_t *out, void *stream);
 
 /* Work schedule of the CTA-pair GEMMs (forward y and backward dX); one
  * setting for the whole process, read once per call. Not part of the method
