@@ -228,6 +228,8 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
   if (x8 != nullptr) {
     if ((s = check_fp8_rows(x8)) != QLORA_OK) return s;
     if (x8->rows != m || x8->cols != red) return QLORA_ERR_SHAPE;
+  } else if (red > kFp8MaxCols) {
+    return QLORA_ERR_SHAPE;      // what check_fp8_rows says of rows in 8 bits
   }
   if (m == 0) return QLORA_OK;
   if ((x_bf16 == nullptr) == (x8 == nullptr) || out_bf16 == nullptr) return QLORA_ERR_INVALID_ARG;

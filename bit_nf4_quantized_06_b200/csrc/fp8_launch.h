@@ -42,6 +42,7 @@ cudaError_t set_fp8_pair_attributes();
 int launch_fp8_split(bool w_mn, const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8Gemm& p, cudaStream_t st);
 cudaError_t set_fp8_split_attributes(int dev);
 constexpr int kFp8MaxSplits = 8;
+constexpr int64_t kFp8MaxCols = int64_t(1) << 30;   // of a row: columns are 32-bit numbers in the kernels
 constexpr int kFp8QuantRows = 4;
 // How many clusters of `splits` CTAs fit on device `dev` at once.
 int fp8_split_clusters(int dev, int splits);

@@ -17,6 +17,7 @@
 
 #include "bulk.cuh"
 #include "fp8_dev.cuh"
+#include "fp8_launch.h"
 #include "host.h"
 #include "ptx.cuh"
 #include "../../include/qlora.h"
@@ -608,7 +609,7 @@ int launch_bwd(const BwdPlan& b, const NormBwd& p, cudaStream_t st) {
 }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxCols = int64_t(1) << 30;    // columns are 32-bit numbers in the kernels
+constexpr int64_t kMaxCols = kFp8MaxCols;
 
 }  // namespace
 

@@ -332,7 +332,7 @@ typedef struct {
 /* Rows (tokens) in 8 bits, caller-owned device buffers. */
 typedef struct {
   int64_t rows;
-  int64_t cols;
+  int64_t cols;    /* 1 to 2^30                                               */
   int64_t ld;      /* bytes from row to row: a multiple of 16, >= cols; bytes
                       past cols are neither read nor written               */
   uint8_t *codes;  /* rows of cols codes, 16-byte aligned                     */
@@ -358,7 +358,8 @@ QLORA_API size_t qlora_fp8_workspace_bytes(int64_t m, int64_t n_out, int64_t k_i
 
 /* y [m x N] bf16 = x W^T. x comes either as bf16 [m x K] (quantized to e4m3
  * rows within the call) or as rows already in 8 bits (x8: m rows of K);
- * exactly one of the two is given. m == 0 is a no-op. */
+ * exactly one of the two is given. m == 0 is a no-op. The reduction (K here, N
+ * for dX) is at most 2^30, in either form of the rows. */
 QLORA_API qlora_status_t qlora_fp8_linear_fwd(const qlora_fp8_t *q, const void *x_bf16, const qlora_fp8_rows_t *x8,
                                               int64_t m, void *y_bf16, void *ws, size_t ws_bytes, void *stream);
 
