@@ -491,6 +491,16 @@ extern "C" qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t* tensors,
     h.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
     h.step_size = static_cast<float>(hp->lr / (1.0 - std::pow(static_cast<double>(hp->beta1), hp->step)));
     h.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(hp->beta2), hp->step)));
+    if (b8 && h.eps < FLT_MIN) {
+      // rcp_approx takes a denominator below the normal numbers for zero, and 0 / eps would be
+      // NaN: the denominator and the step size both times 2^30, which rounds nothing (roots are
+      // at most 2^64 and their correction below 2^13)
+      constexpr float kUp = 1073741824.0f;
+      h.eps *= kUp;
+      h.inv_sqrt_bc2 *= kUp;
+      h.step_size *= kUp;
+      if (!std::isfinite(h.step_size)) return QLORA_ERR_INVALID_ARG;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // as many tensors a launch as its parameter block and 31-bit chunk numbers hold
     for (size_t at = 0; at < live.size();) {

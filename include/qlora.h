@@ -418,7 +418,8 @@ QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void *dy_bf16, const void *h_bf
  *     needs. A gradient that is not finite spoils its own value only, as with
  *     32-bit states: its codes are NaN and stay out of amax. The step itself
  *     uses the new m and r before they are rounded to 8 bits; its quotient
- *     m / (r / sqrt(1 - b2^t) + eps) is off by 2^-21 of itself at most.
+ *     m / (r / sqrt(1 - b2^t) + eps) is off by 2^-21 of itself at most. (With an
+ *     eps below 2^-126, lr / (1 - b1^t) above 2^97 is refused.)
  * `tensors` is a host array; it is read during the call (a captured call
  * keeps the pointers and the step number that it was captured with) and may
  * be reused at once. All buffers are device memory (states in pinned host
