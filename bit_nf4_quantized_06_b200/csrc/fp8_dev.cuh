@@ -34,8 +34,9 @@ __device__ __forceinline__ float fp8_mag(float v) {
   return a <= FLT_MAX ? a : 0.0f;
 }
 
-// The value to convert: v * inv, or NaN where v is not finite (v - v is then NaN, else 0).
-__device__ __forceinline__ float fp8_scaled(float v, float inv) { return fmaf(v, inv, v - v); }
+// The value to convert: v * inv, or NaN where v is not finite (v - v is then NaN,
+// else 0; a negative zero added leaves a product of either sign as it is).
+__device__ __forceinline__ float fp8_scaled(float v, float inv) { return fmaf(v, inv, -(v - v)); }
 
 // Two values to codes (lo in the low byte): round to nearest even, saturate, NaN stays NaN.
 template <int FMT>

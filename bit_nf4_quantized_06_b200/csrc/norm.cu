@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(NV == 0 ? 1024 : 512) k_rows_fwd(NormFwd p) {
       const uint32_t tw[4] = {t.x, t.y, t.z, t.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[2 * i] = fma_lo(tw[i], gw[i], 0.0f) * rstd;
-        f[2 * i + 1] = fma_hi(tw[i], gw[i], 0.0f) * rstd;
+        f[2 * i] = fma_lo(tw[i], gw[i], -0.0f) * rstd;        // -0: a product of zero keeps its sign
+        f[2 * i + 1] = fma_hi(tw[i], gw[i], -0.0f) * rstd;
       }
     } else {
       unpack8(t, f);

@@ -310,6 +310,7 @@ QLORA_API qlora_status_t qlora_adamw_staged(float *master, void *param_bf16, con
  *   amax  = max over the block's finite |v|, at least 2^-100
  *   scale = fl32(amax / F)
  *   code  = fp8_rn(clamp(fl32(v * fl32(F / amax)), -F, F))
+ * Zeros, and values that round to zero, keep their sign.
  * An infinite or NaN value becomes the NaN code and does not enter amax, so
  * it spoils only the results that it takes part in.
  *   weight: 128 x 128 blocks, e4m3; the last blocks of either axis are short

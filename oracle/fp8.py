@@ -54,10 +54,10 @@ def block_scale(v, fmt, axis=-1):
 
 
 def scaled(v, inv):
-    """fl32(v inv) where v is finite, else NaN; zeros come out positive."""
+    """fl32(v inv) where v is finite, else NaN; zeros keep their sign."""
     v = np.asarray(v, np.float32)
     with np.errstate(invalid="ignore", over="ignore"):
-        return np.where(np.isfinite(v), v * inv + np.float32(0), np.float32(np.nan)).astype(np.float32)
+        return np.where(np.isfinite(v), v * inv, np.float32(np.nan)).astype(np.float32)
 
 
 def quantize_rows(x, fmt, block=128):
