@@ -100,7 +100,8 @@ struct DevState {
   bool attrs = false;      // kernel attributes set in context `ctx`
   CUcontext ctx = nullptr;
   int pair_clusters = 0;   // CTA pairs of k_tc_pair that can be resident at once
-  unsigned int* status = nullptr;   // g_dev_status in context `ctx`
+  unsigned int* status = nullptr;   // g_dev_status in context `ctx`, for kernels that get it as an argument
+  unsigned families = 0;   // a bit an OpFamily whose kernels' attributes are set in context `ctx`
 };
 std::mutex g_mu;
 DevState g_dev[64];
@@ -228,13 +229,10 @@ qlora_status_t device_ready(int* sms_out, int* pairs_out = nullptr) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_merge_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(merge_tc_smem_bytes()));
-    if (e == cudaSuccess) e = set_fp8_attributes(dev);
-    if (e == cudaSuccess) e = set_norm_attributes();
-    if (e == cudaSuccess) e = set_adamw_attributes();
-    if (e == cudaSuccess) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&st.status), g_dev_status);
     if (e != cudaSuccess) return QLORA_ERR_CUDA;
     st.attrs = true;
     st.ctx = ctx;
+    st.families = 0;
   }
   if (sms_out) *sms_out = st.sms;
   if (pairs_out) *pairs_out = st.pair_clusters;
@@ -252,7 +250,29 @@ unsigned int* device_status_word() {
   std::lock_guard<std::mutex> lk(g_mu);
   return g_dev[dev].status;
 }
-int check_current_device(int* sms, int* pairs) { return static_cast<int>(device_ready(sms, pairs)); }
+int check_current_device(OpFamily family, int* sms, int* pairs) {
+  const qlora_status_t s = device_ready(sms, pairs);
+  if (s != QLORA_OK) return static_cast<int>(s);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return static_cast<int>(QLORA_ERR_CUDA);
+  std::lock_guard<std::mutex> lk(g_mu);
+  DevState& st = g_dev[dev];
+  const unsigned bit = 1u << static_cast<int>(family);
+  if (!(st.families & bit)) {
+    cudaError_t e = cudaSuccess;
+    switch (family) {
+      case OpFamily::kFp8:
+        e = set_fp8_attributes(dev);
+        if (e == cudaSuccess) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&st.status), g_dev_status);
+        break;
+      case OpFamily::kNorm: e = set_norm_attributes(); break;
+      case OpFamily::kAdamw: e = set_adamw_attributes(); break;
+    }
+    if (e != cudaSuccess) return static_cast<int>(QLORA_ERR_CUDA);
+    st.families |= bit;
+  }
+  return static_cast<int>(QLORA_OK);
+}
 
 namespace {
 

@@ -235,7 +235,7 @@ qlora_status_t product(const qlora_fp8_t* q, const void* x_bf16, const qlora_fp8
   if ((x_bf16 == nullptr) == (x8 == nullptr) || out_bf16 == nullptr) return QLORA_ERR_INVALID_ARG;
   if (!aligned(x_bf16, 16) || !aligned(out_bf16, 16) || !aligned(ws, 16)) return QLORA_ERR_ALIGNMENT;
   int sms = 0, pairs = 0;
-  if ((s = static_cast<qlora_status_t>(check_current_device(&sms, &pairs))) != QLORA_OK) return s;
+  if ((s = static_cast<qlora_status_t>(check_current_device(OpFamily::kFp8, &sms, &pairs))) != QLORA_OK) return s;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_CUDA;
   qlora_fp8_rows_t rows;
@@ -277,7 +277,7 @@ qlora_status_t qlora_quantize_fp8(const void* w_bf16, const qlora_fp8_t* q, void
   const int64_t blocks = cdiv(q->n_out, kFp8Block) * cdiv(q->k_in, kFp8Block);
   if (blocks > kMaxDim) return QLORA_ERR_SHAPE;
   int sms = 0;
-  if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
+  if ((s = static_cast<qlora_status_t>(check_current_device(OpFamily::kFp8, &sms))) != QLORA_OK) return s;
   return static_cast<qlora_status_t>(host::launch_pdl(
       k_quantize_fp8, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream), 1,
       static_cast<const __nv_bfloat16*>(w_bf16), q->codes, q->scales, q->n_out, q->k_in));
@@ -289,7 +289,7 @@ qlora_status_t qlora_dequantize_fp8(const qlora_fp8_t* q, void* w_bf16_out, void
   if (w_bf16_out == nullptr) return QLORA_ERR_INVALID_ARG;
   if (!aligned(w_bf16_out, 16)) return QLORA_ERR_ALIGNMENT;
   int sms = 0;
-  if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
+  if ((s = static_cast<qlora_status_t>(check_current_device(OpFamily::kFp8, &sms))) != QLORA_OK) return s;
   const int64_t blocks = std::min<int64_t>(cdiv(q->n_out * (q->k_in / 8), 256), int64_t(sms) * 8);
   return static_cast<qlora_status_t>(host::launch_pdl(
       k_dequantize_fp8, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream), 1,
@@ -300,7 +300,7 @@ qlora_status_t qlora_dequantize_fp8(const qlora_fp8_t* q, void* w_bf16_out, void
 size_t qlora_fp8_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in) {
   if (m < 1 || m > kMaxDim || n_out < 1 || n_out > kMaxDim || k_in < 1 || k_in > kMaxDim || k_in % 16 != 0) return 0;
   int dev = 0, sms = 0, pairs = 0;
-  if (m <= kFp8QuantRows && check_current_device(&sms, &pairs) == QLORA_OK && cudaGetDevice(&dev) == cudaSuccess &&
+  if (m <= kFp8QuantRows && check_current_device(OpFamily::kFp8, &sms, &pairs) == QLORA_OK && cudaGetDevice(&dev) == cudaSuccess &&
       quantizes(m, n_out, k_in, dev, pairs) && quantizes(m, k_in, n_out, dev, pairs))
     return 0;
   return std::max(plan_product(m, k_in).total, plan_product(m, n_out).total);

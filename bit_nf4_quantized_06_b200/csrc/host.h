@@ -9,22 +9,23 @@
 
 namespace qlora {
 
+// Operators whose kernels' attributes are set together, by the first call of
+// one of them in a context: nobody else's first call pays for it (all three
+// together took a first NF4 call from 7.0 to 7.8 ms) or fails with it.
+enum class OpFamily : int { kFp8 = 0, kNorm = 1, kAdamw = 2 };
+
 // Device check of the current device (see check_current_device_status), with
 // its SM count and how many CTA pairs of one CTA a SM fit on it at once.
-int check_current_device(int* sms, int* pairs = nullptr);
+int check_current_device(OpFamily family, int* sms, int* pairs = nullptr);
 
-// Shared-memory limits of the 8-bit product's kernels (fp8.cu); part of the
-// device check, which sets every kernel's attributes once a context.
-cudaError_t set_fp8_attributes(int dev);
-
-// The same for the RMS norm's (norm.cu).
-cudaError_t set_norm_attributes();
-
-// And the many-tensor AdamW's (optim_multi.cu).
-cudaError_t set_adamw_attributes();
+// What the check does for each family: the shared-memory limits of its kernels,
+// and how many clusters of the 8-bit product's split kernel fit on the device.
+cudaError_t set_fp8_attributes(int dev);    // fp8.cu
+cudaError_t set_norm_attributes();          // norm.cu
+cudaError_t set_adamw_attributes();         // optim_multi.cu
 
 // Device address of the status word (ptx.cuh) on the current device, after a
-// successful device check.
+// successful device check of the 8-bit product's family.
 unsigned int* device_status_word();
 
 // Counts a launch and returns its status (a qlora_status_t).

@@ -660,7 +660,7 @@ qlora_status_t qlora_quantize_fp8_rows(const void* x_bf16, const qlora_fp8_rows_
   if (x_bf16 == nullptr) return QLORA_ERR_INVALID_ARG;
   if (!aligned(x_bf16, 16)) return QLORA_ERR_ALIGNMENT;
   int sms = 0;
-  if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
+  if ((s = static_cast<qlora_status_t>(check_current_device(OpFamily::kNorm, &sms))) != QLORA_OK) return s;
   return static_cast<qlora_status_t>(launch_quantize_rows(x_bf16, *out, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -682,7 +682,7 @@ qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, 
       !aligned(y_bf16, 16) || !aligned(rstd_out, 4))
     return QLORA_ERR_ALIGNMENT;
   int sms = 0;
-  const qlora_status_t s = static_cast<qlora_status_t>(check_current_device(&sms));
+  const qlora_status_t s = static_cast<qlora_status_t>(check_current_device(OpFamily::kNorm, &sms));
   if (s != QLORA_OK) return s;
   NormFwd p{};
   p.x = static_cast<const __nv_bfloat16*>(x_bf16);
@@ -708,7 +708,7 @@ qlora_status_t qlora_rmsnorm_fwd(const void* x_bf16, const void* residual_bf16, 
 size_t qlora_rmsnorm_workspace_bytes(int64_t rows, int64_t d) {
   if (rows < 1 || rows > kMaxRows || d < 1 || d > kMaxCols) return 0;
   int sms = 0;
-  if (check_current_device(&sms) != QLORA_OK) sms = 148;
+  if (check_current_device(OpFamily::kNorm, &sms) != QLORA_OK) sms = 148;
   return static_cast<size_t>(plan_bwd(rows, d, sms).grid) * static_cast<size_t>(d) * sizeof(float);
 }
 
@@ -723,7 +723,7 @@ qlora_status_t qlora_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const 
   const dim3 rblock(32, 32), rgrid(static_cast<unsigned>(cdiv(d, 32)));
   if (rows == 0) {
     if (dgamma == nullptr) return QLORA_OK;
-    if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
+    if ((s = static_cast<qlora_status_t>(check_current_device(OpFamily::kNorm, &sms))) != QLORA_OK) return s;
     return static_cast<qlora_status_t>(
         host::launch_pdl(k_dgamma, rgrid, rblock, 0, st, 1, static_cast<const float*>(nullptr), 0, d, dgamma));
   }
@@ -732,7 +732,7 @@ qlora_status_t qlora_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const 
   if (!aligned(dy_bf16, 16) || !aligned(h_bf16, 16) || !aligned(gamma_bf16, 16) || !aligned(rstd, 4) ||
       !aligned(dres_bf16, 16) || !aligned(dx_bf16, 16) || !aligned(ws, 16))
     return QLORA_ERR_ALIGNMENT;
-  if ((s = static_cast<qlora_status_t>(check_current_device(&sms))) != QLORA_OK) return s;
+  if ((s = static_cast<qlora_status_t>(check_current_device(OpFamily::kNorm, &sms))) != QLORA_OK) return s;
   const BwdPlan b = plan_bwd(rows, d, sms);
   if (dgamma != nullptr && (ws == nullptr || ws_bytes < static_cast<size_t>(b.grid) * d * sizeof(float)))
     return QLORA_ERR_WORKSPACE;

@@ -481,7 +481,7 @@ extern "C" qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t* tensors,
         overlap(live, [&](int i) { return addr(tensors[i].v); }, [&](int i) { return w * n(i); }))
       return QLORA_ERR_INVALID_ARG;
     int sms = 0;
-    qlora_status_t s = static_cast<qlora_status_t>(check_current_device(&sms));
+    qlora_status_t s = static_cast<qlora_status_t>(check_current_device(OpFamily::kAdamw, &sms));
     if (s != QLORA_OK) return s;
     // step constants in double, rounded once, as qlora_adamw_step has them
     AdamwHyper h{};
