@@ -23,7 +23,7 @@ int launch_quantize_rows(const void* x_bf16, const qlora_fp8_rows_t& out, int sm
 namespace {
 
 // ------------------------------------------------------------------ weight quantizer
-// One CTA per 128 x 128 block: 8 values a thread and step, 16 steps, kept in
+// One CTA per 128 x 128 block: 8 values a thread and step, eight steps, kept in
 // registers between the maximum and the codes. Bound by HBM (3 bytes a value).
 __global__ void __launch_bounds__(256) k_quantize_fp8(const __nv_bfloat16* __restrict__ w, uint8_t* __restrict__ codes,
                                                       float* __restrict__ scales, int64_t n, int64_t k) {
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) k_quantize_fp8(const __nv_bfloat16* __res
   }
 }
 
-// bf16(code * scale), eight values a thread; rows over blockIdx.y and on.
+// bf16(code * scale), eight values a thread and step, the weight as one list.
 __global__ void __launch_bounds__(256) k_dequantize_fp8(const uint8_t* __restrict__ codes,
                                                         const float* __restrict__ scales, __nv_bfloat16* __restrict__ w,
                                                         int64_t n, int64_t k) {

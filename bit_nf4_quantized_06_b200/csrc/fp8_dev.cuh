@@ -1,5 +1,6 @@
 // Block quantization to 8-bit floating point, shared by every kernel that
-// writes codes:
+// writes codes of weights or rows (the optimizer's states have a scale and an
+// inverse of their own, optim_multi.cu):
 //   amax  = max over the block's finite |v|, at least 2^-100
 //   scale = fl32(amax / F),  F = 448 (e4m3) or 57344 (e5m2)
 //   code  = fp8_rn(clamp(fl32(v * fl32(F / amax)), -F, F)), NaN unless v is finite

@@ -24,11 +24,14 @@
 // Measured, 4096 rows x 11008 outputs x 4096: 189 us, 1.95 PFLOP/s, at the
 // board's 1000 W limit (SM clock 1.6 of 1.965 GHz; single launches with pauses
 // 166 us); dX of the same weight 200 us with the rows' quantizer. A block takes
-// some 890 cycles: its sums are ready 740 after the issue (512 of them MMA),
-// the epilogue warps then take 450 to read them back and free the buffer, and
-// with two buffers the tensor core waits for that. The FMAs are a third of it
-// (taken out in a copy: 690 cycles, where the operands' way from L2, 50 bytes a
-// clock and SM, is the next bound). On the way: scales read by the epilogue
+// some 890 cycles, where the tensor core needs 512. Its sums are ready 740 after
+// the issue, and the epilogue warps take 450 to read them back and free the
+// buffer: with two buffers that alone would allow a block every 595 cycles, so
+// it is not what holds the kernel by itself. With the epilogue's FMAs taken out
+// in a copy a block still takes 690: the operands' way (L2 at 50 bytes a clock
+// and SM, then load, MMA and release through four stages) holds it there, and
+// the epilogue costs the other 200. How many stages would shorten the first part
+// was not measured. On the way: scales read by the epilogue
 // warps themselves 275 us; sixteen epilogue warps and one line of shared memory a
 // scale 222; eight with 216 registers 211; barrier waits taken ahead 192; a
 // chunk's scales read at once 190, the MMA's thread spinning 189. Not kept, all slower: tiles of 160 outputs
@@ -124,8 +127,8 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
   grid_dependency_wait();
   grid_dependency_trigger();
 
-  // registers move from the first warpgroup to the epilogue's four (both
-  // sides' sum stays below the launch's)
+  // registers move from the first warpgroup to the epilogue's two (the three
+  // shares' sum stays below the launch's)
   if (warp < 4) setmaxnreg_dec<kFp8PairIssueRegs>();
   if (warp == 0) {
     if (lane == 0) {
@@ -189,10 +192,10 @@ __global__ void __launch_bounds__(kFp8PairThreads, 1)
     }
     __syncwarp();
   } else if (warp < 4) {
-    // scales: chunks of eight reduction blocks, slot [block][128 rows, two
-    // weight blocks]; read along the blocks (32 bytes a row), written along
-    // the rows, so that an epilogue warp's scales are one shared-memory line.
-    // A chunk is requested while the one before is at work: its loads wait in
+    // scales: chunks of eight reduction blocks, a slot holding each row's eight
+    // together and then the two weight blocks' eight each; a warp reads four
+    // rows of eight at a time from memory, and an epilogue thread its row's
+    // eight in two 16-byte loads. A chunk is requested while the one before is at work: its loads wait in
     // registers for the slot (requested only once the slot was free, they held
     // the epilogue up by 320 to 700 cycles a block).
     const int half = warp - 2;                  // rows [64 half, 64 half + 64)

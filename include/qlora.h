@@ -317,8 +317,9 @@ QLORA_API qlora_status_t qlora_adamw_staged(float *master, void *param_bf16, con
  *   rows:   blocks of 128 consecutive columns of one row, e4m3 or e5m2
  * Products of codes are summed in fp32 within a block of 128 of the
  * reduction, multiplied by the two scales, and summed over blocks in fp32, in
- * a fixed order: results repeat bit for bit. The output overlaps no other
- * buffer. Calls that can overlap on the GPU (on two streams, in two graphs)
+ * an order that the sizes and the device fix: a call of equal sizes repeats bit
+ * for bit, while a row's last bits may differ between calls with more or fewer
+ * rows around it. The output overlaps no other buffer. Calls that can overlap on the GPU (on two streams, in two graphs)
  * need workspaces of their own, here and for qlora_rmsnorm_bwd. */
 typedef enum { QLORA_FP8_E4M3 = 0, QLORA_FP8_E5M2 = 1 } qlora_fp8_format_t;
 
@@ -380,8 +381,11 @@ QLORA_API qlora_status_t qlora_fp8_linear_bwd(const qlora_fp8_t *q, const void *
  * as 8-bit rows for qlora_fp8_linear_fwd, to y8 (e4m3 or e5m2); exactly one is
  * given. h_out [rows x d] bf16 receives h where there is a residual (NULL
  * without one); it may be x's or the residual's own buffer. rstd_out [rows]
- * may be NULL. No other buffers may overlap. rows == 0 is a no-op; d >= 1;
- * eps >= 0 and finite. A row of zeros with eps 0 gives NaN, as the formula. */
+ * may be NULL. No other buffers may overlap. rows == 0 is a no-op; d from 1 to
+ * 2^30; eps >= 0 and finite. A row of zeros with eps 0 gives NaN, as the
+ * formula. The sum of squares is fp32, off by (max(32, d / 2048) + 12) 2^-24
+ * of itself at most, in an order that d, the device and whether there are few
+ * rows fix; where it passes fp32's range rstd is 0. */
 QLORA_API qlora_status_t qlora_rmsnorm_fwd(const void *x_bf16, const void *residual_bf16, const void *gamma_bf16,
                                            int64_t rows, int64_t d, float eps, void *h_out_bf16, void *y_bf16,
                                            const qlora_fp8_rows_t *y8, float *rstd_out, void *stream);
@@ -394,7 +398,10 @@ QLORA_API size_t qlora_rmsnorm_workspace_bytes(int64_t rows, int64_t d);
  *   dgamma [d] fp32    = sum over rows of dy h rstd (overwritten; NULL to skip)
  * dres [rows x d] bf16, the gradient that reaches h past the norm, may be
  * NULL; dx is the gradient of x and of the residual alike and may be dres's or
- * dy's own buffer. Sums run in a fixed order: results repeat bit for bit.
+ * dy's own buffer. Sums run in an order that the sizes and the device fix: a
+ * call of equal sizes repeats bit for bit. They are fp32: a row's sum is off by
+ * (max(32, d / 512) + 12) 2^-24 of its terms' magnitudes at most, dgamma by
+ * (rows + 8) 2^-24.
  * rows == 0 zeroes dgamma. */
 QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void *dy_bf16, const void *h_bf16, const void *gamma_bf16,
                                            const float *rstd, const void *dres_bf16, int64_t rows, int64_t d,
@@ -424,10 +431,11 @@ QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void *dy_bf16, const void *h_bf
  * `tensors` is a host array; it is read during the call (a captured call
  * keeps the pointers and the step number that it was captured with) and may
  * be reused at once. All buffers are device memory (states in pinned host
- * memory stay with qlora_adamw_step and _staged). Buffers of different tensors must not overlap: the same master, m or
- * v twice is refused. n == 0 entries are skipped. fp32 pointers 4-byte,
- * param_bf16 (may be NULL) 2-byte aligned; tensors with 16-byte aligned
- * buffers (8-byte for bf16 and codes) take the wide loads. */
+ * memory stay with qlora_adamw_step and _staged). Buffers of different tensors
+ * must not overlap: the same master, m or v twice is refused. n == 0 entries
+ * are skipped. fp32 pointers 4-byte, param_bf16 (may be NULL) 2-byte aligned;
+ * tensors whose master, grad, m and v (codes too) are 16-byte aligned, and
+ * param_bf16 8-byte, take the wide copies, others one value at a time. */
 typedef struct {
   float *master;
   void *param_bf16;
