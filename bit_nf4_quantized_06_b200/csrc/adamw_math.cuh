@@ -11,6 +11,7 @@ struct AdamwHyper {
   float decay;              // 1 - lr * weight_decay
   float step_size;          // lr / (1 - beta1^t)
   float inv_sqrt_bc2;       // 1 / sqrt(1 - beta2^t)
+  float one;                // 1, which the compiler does not know (the 8-bit states' sums)
 };
 
 // m, v become the new states, root = sqrt(v); returns the new parameter.

@@ -7,7 +7,7 @@
 //
 // 8 bits: m and sqrt(v) are e4m3 codes with one fp32 scale per 256 values of
 // a tensor; a warp owns a block, eight values a lane, so that
-// the block's maxima are warp shuffles. sqrt(v) rather than v: e4m3 spans
+// the block's maxima are one warp operation each. sqrt(v) rather than v: e4m3 spans
 // 2^17.8 from its smallest code to its largest, which is 2^35 of v. A code of
 // a value above zero is not allowed to become zero, else the next step would
 // divide by eps alone. The step uses the new m and v in fp32, so rounding
@@ -90,23 +90,29 @@ __device__ __forceinline__ float hi_of(uint64_t v) {
   return __uint_as_float(b);
 }
 
-// a x + b y in pairs, each product and the sum rounded by itself. The assembler
-// joins a packed product and a packed sum into one fused operation, `.rn` or
-// not; these scalar forms it leaves as they are.
-__device__ __forceinline__ uint64_t sum_apart(float a, uint64_t x, float b, uint64_t y) {
-  return f2(__fadd_rn(__fmul_rn(a, lo_of(x)), __fmul_rn(b, lo_of(y))),
-            __fadd_rn(__fmul_rn(a, hi_of(x)), __fmul_rn(b, hi_of(y))));
-}
-
 // Constants of the 8-bit step; the update's in pairs.
 struct Hyper2 {
-  float beta1, gain1, beta2, gain2;
+  float beta1, gain1, beta2, gain2, one;
   uint64_t decay, neg_step, inv_sqrt_bc2, eps;
 };
 __device__ __forceinline__ Hyper2 hyper2(const AdamwHyper& a) {
   auto two = [](float v) { return f2(v, v); };
-  return Hyper2{a.beta1,      1.0f - a.beta1,      a.beta2,           1.0f - a.beta2,
+  return Hyper2{a.beta1,      1.0f - a.beta1,    a.beta2,             1.0f - a.beta2, a.one,
                 two(a.decay), two(-a.step_size), two(a.inv_sqrt_bc2), two(a.eps)};
+}
+
+// a x + b y in pairs, each product and the sum rounded by itself. The assembler
+// joins a packed product and a packed sum into one fused operation, `.rn` or
+// not; a sum as x * one + y, with a one that it does not know, it leaves as it is.
+__device__ __forceinline__ uint64_t sum_apart(float a, uint64_t x, float b, uint64_t y, float one) {
+  return f2_fma(f2_mul(f2(a, a), x), f2(one, one), f2_mul(f2(b, b), y));
+}
+
+// The largest of a warp's values, NaN aside.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // Where a block's values lie in a stage; p == 0: nowhere.
@@ -168,9 +174,9 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
     const float2 mm = fp8_unpack2<kE4M3>((j < 4 ? mq.x : mq.y) >> sh);
     const float2 rr = fp8_unpack2<kE4M3>((j < 4 ? vq.x : vq.y) >> sh);
     const uint64_t g2 = f2(g[j], g[j + 1]);
-    const uint64_t m2 = sum_apart(hp.beta1, f2_mul(f2(mm.x, mm.y), ms2), hp.gain1, g2);
+    const uint64_t m2 = sum_apart(hp.beta1, f2_mul(f2(mm.x, mm.y), ms2), hp.gain1, g2, hp.one);
     const uint64_t r2 = f2_mul(f2(rr.x, rr.y), vs2);
-    const uint64_t v2 = sum_apart(hp.beta2, f2_mul(r2, r2), hp.gain2, f2_mul(g2, g2));
+    const uint64_t v2 = sum_apart(hp.beta2, f2_mul(r2, r2), hp.gain2, f2_mul(g2, g2), hp.one);
     r[j] = __fsqrt_rn(lo_of(v2));
     r[j + 1] = __fsqrt_rn(hi_of(v2));
     const uint64_t d2 = f2_fma(f2(r[j], r[j + 1]), hp.inv_sqrt_bc2, hp.eps);
@@ -183,11 +189,8 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
     am = fmaxf(am, fmaxf(fabsf(m[j]), fabsf(m[j + 1])));
     av = fmaxf(av, fmaxf(r[j], r[j + 1]));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-    av = fmaxf(av, __shfl_xor_sync(0xFFFFFFFFu, av, o));
-  }
+  am = warp_max(am);
+  av = warp_max(av);
   if (fmaxf(am, av) > FLT_MAX) {               // the same for the whole warp: infinities become NaN
     am = av = 0.0f;
 #pragma unroll
@@ -197,21 +200,20 @@ __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane
       m[j] += m[j] - m[j];
       r[j] += r[j] - r[j];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-      av = fmaxf(av, __shfl_xor_sync(0xFFFFFFFFu, av, o));
-    }
+    am = warp_max(am);
+    av = warp_max(av);
   }
   constexpr float F = 448.0f;
   am = fmaxf(am, kFp8Least);
   av = fmaxf(av, kFp8Least);
   const float im = F * __frcp_rn(am), iv = F * __frcp_rn(av);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] *= im;
-    const float c = r[j] * iv;
-    r[j] = r[j] > 0.0f ? fmaxf(c, kLeastRoot) : c;
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t cm = f2_mul(f2(m[j], m[j + 1]), f2(im, im)), cr = f2_mul(f2(r[j], r[j + 1]), f2(iv, iv));
+    m[j] = lo_of(cm);
+    m[j + 1] = hi_of(cm);
+    r[j] = r[j] > 0.0f ? fmaxf(lo_of(cr), kLeastRoot) : lo_of(cr);
+    r[j + 1] = r[j + 1] > 0.0f ? fmaxf(hi_of(cr), kLeastRoot) : hi_of(cr);
   }
   mq = make_uint2(fp8_pack4<kE4M3>(m[0], m[1], m[2], m[3]), fp8_pack4<kE4M3>(m[4], m[5], m[6], m[7]));
   vq = make_uint2(fp8_pack4<kE4M3>(r[0], r[1], r[2], r[3]), fp8_pack4<kE4M3>(r[4], r[5], r[6], r[7]));
@@ -488,6 +490,7 @@ extern "C" qlora_status_t qlora_adamw_multi(const qlora_adamw_tensor_t* tensors,
     h.beta1 = hp->beta1;
     h.beta2 = hp->beta2;
     h.eps = hp->eps;
+    h.one = 1.0f;
     h.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
     h.step_size = static_cast<float>(hp->lr / (1.0 - std::pow(static_cast<double>(hp->beta1), hp->step)));
     h.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(hp->beta2), hp->step)));
