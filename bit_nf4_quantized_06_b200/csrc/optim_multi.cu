@@ -25,7 +25,8 @@
 // bits). A CTA takes chunks of eight blocks, a block a warp, through a ring of
 // stages in shared memory: one stage holds a chunk's master values, gradients
 // and states, filled by four bulk copies that are requested several chunks
-// ahead. Measured, 8 bits, 160 million values in 448 tensors: 466 us, 6.2 TB/s
+// ahead. Measured, 8 bits, 160 million values in 448 tensors: 450 us, 6.4 TB/s,
+// in runs of hundreds of steps, at the board's power limit, 475 to 500
 // (loads to registers kept 61 KB in flight on an SM, 573 us; a ring a warp, of
 // 256-byte copies, was bound by the copies' number, 816 us); 32 bits, 134
 // million values: 688 us, 5.9 TB/s.
@@ -126,12 +127,12 @@ __device__ __forceinline__ int value_of(int lane, int j) { return (j >> 2) * 128
 
 // The 8-bit step of the block at i0 (`src`: its stage, or 0 for plain
 // accesses; `read` is called once its values are in registers, and says whether
-// they may be used), in packed pairs. The states' operations are rounded one by one (the square root's share
-// is 22 us of 466 for 160 million values; with the hardware's approximate one
-// states were not reproducible). The update's reciprocal, which no state
-// depends on, is the hardware's, off by one step of fp32 at most: with a
-// rounded quotient too this kernel was bound by issue (83 instructions a value,
-// 654 us).
+// they may be used), in packed pairs. The states' operations are rounded one by
+// one; the rounded square root takes 20 to 30 us more of 160 million values than
+// the hardware's approximate one, with which states were not reproducible. The
+// update's reciprocal, which no state depends on, is the hardware's, off by one
+// step of fp32 at most: with a rounded quotient too this kernel was bound by
+// issue (83 instructions a value, 654 us).
 template <typename Read>
 __device__ __forceinline__ void step8(const MultiTensor& t, int64_t i0, int lane, const Stage& src, const Hyper2& hp,
                                       Read read) {
