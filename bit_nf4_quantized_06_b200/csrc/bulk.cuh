@@ -68,8 +68,10 @@ struct BulkRing {
   // The filler, last of all: nothing to do unless a wait gave up. Bounded; false
   // if copies are still under way.
   __device__ __forceinline__ bool drain(uint64_t limit_ns = QLORA_WAIT_LIMIT_NS) const {
+    uint32_t left = lds_u1(bars - 8) ^ phases;
+    if (left == 0) return true;
     const uint64_t t0 = globaltimer_ns();
-    for (uint32_t left = lds_u1(bars - 8) ^ phases; left != 0; left &= left - 1) {
+    for (; left != 0; left &= left - 1) {
       const int s = __ffs(left) - 1;
       while (!mbar_try_wait(bar(s), (phases >> s) & 1))
         if (globaltimer_ns() - t0 > limit_ns) return false;
